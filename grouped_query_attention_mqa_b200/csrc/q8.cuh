@@ -1,0 +1,79 @@
+// Shared pieces of the 8-bit K/V cache: conversions between fp32 and e4m3,
+// row scales, and the arguments of the kernels over such caches.
+//
+// A cached row of one K/V head is d e4m3 codes and an exponent byte E; its
+// values are code * s with s the fp32 number whose exponent field is E and
+// whose mantissa is 0 (a power of two; 0 for E = 0).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "mqa_q8.h"
+
+namespace mqa {
+namespace q8 {
+
+constexpr float kCodeMax = 448.f;   // largest e4m3 value
+
+__device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
+
+// Exponent byte of a row whose largest finite magnitude is `amax`: the
+// smallest s with amax <= 448 s.  448 = 1.75 * 2^8, so with amax = 1.m * 2^k
+// s is 2^(k-8), or 2^(k-7) when 1.m > 1.75.  Zero and subnormal maxima clamp
+// to the smallest normal s (E = 1).
+__device__ __forceinline__ uint32_t exponent_for(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = int(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return uint32_t(e < 1 ? 1 : e);
+}
+
+// 1 / scale_of(E) for E from exponent_for (1..247), exact.
+__device__ __forceinline__ float inverse_scale(uint32_t e) { return __uint_as_float((254u - e) << 23); }
+
+// Two fp32 -> two e4m3 codes (x0 in the low byte), nearest even, saturating at
+// +-448; NaN stays NaN.
+__device__ __forceinline__ uint32_t to_e4m3x2(float x0, float x1) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
+  return r;
+}
+
+// Two e4m3 codes (low 16 bits of w) -> two fp32, exact.
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(w)));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// Attention over an 8-bit cache.
+struct DecodeQ8Args {
+  void* o;
+  const void* q;
+  const uint8_t* k;    // [b, m_max, g, d_k] codes
+  const uint8_t* ke;   // [b, g, m_max] exponents
+  const uint8_t* v;
+  const uint8_t* ve;
+  const int32_t* lens;
+  int b, h, g, m_max, d_k, d_v, hq;
+  int window;          // 0: all rows
+  int no_merge;        // no segment spans two tiles: every output row is written by the decode itself
+  float scale;
+  Workspace ws;
+  int32_t* flags;
+  int grid;
+};
+
+cudaError_t launch_q8_append(uint8_t* k, uint8_t* ke, uint8_t* v, uint8_t* ve, const void* k_new, const void* v_new,
+                             const int32_t* pos, const int32_t* cu, int b, int total, int m_max, int g, int d_k,
+                             int d_v, mqa_dtype_t dtype, int32_t* flags, cudaStream_t stream);
+cudaError_t launch_q8_read(void* k_out, void* v_out, const uint8_t* k, const uint8_t* ke, const uint8_t* v,
+                           const uint8_t* ve, const int32_t* start, const int32_t* cu, int b, int total, int m_max,
+                           int g, int d_k, int d_v, mqa_dtype_t dtype, int32_t* flags, cudaStream_t stream);
+
+cudaError_t launch_q8_decode_simt(const DecodeQ8Args& a, mqa_dtype_t dtype, cudaStream_t stream);
+int q8_simt_ctas_per_sm(int d_k, int d_v, int hq);
+int q8_simt_tile_rows();
+
+}  // namespace q8
+}  // namespace mqa
