@@ -71,6 +71,38 @@ cudaError_t launch_q8_read(void* k_out, void* v_out, const uint8_t* k, const uin
                            const uint8_t* ve, const int32_t* start, const int32_t* cu, int b, int total, int m_max,
                            int g, int d_k, int d_v, mqa_dtype_t dtype, int32_t* flags, cudaStream_t stream);
 
+// The tensor-core kernel's view of a batch: `nseq` row lists ("sequences"),
+// each of g segments (one per K/V head) with up to `cols` query columns.
+// A plain decode: one list per sequence.  A shared prefix: first `nblk` lists
+// that are the prefix, each for `spb` sequences' queries, then one list per
+// sequence for its own rows.
+struct TcArgs {
+  void* o;
+  const __nv_bfloat16* q;
+  const uint8_t* ke;     // exponents [b, g, m]
+  const uint8_t* ve;
+  const int32_t* lens;   // [b]
+  const uint8_t* pke;    // prefix exponents [g, m_p]
+  const uint8_t* pve;
+  const int32_t* plen;   // [1]
+  int b, h, g, hq, m, m_p;
+  int window, no_merge;
+  int nseq, nblk, spb, cols;
+  float scale;
+  Workspace ws;
+  int32_t* flags;
+  int grid;
+};
+
+bool q8_tc_supported(int d_k, int d_v, int hq);
+int q8_tc_tile_rows(int hq);
+cudaError_t launch_q8_decode_tc(const DecodeQ8Args& a, cudaStream_t stream);
+// Prefix and own rows of a whole batch, and the merge.
+cudaError_t launch_q8_decode_shared(const TcArgs& a, const uint8_t* pk, const uint8_t* pv, const uint8_t* k,
+                                    const uint8_t* v, cudaStream_t stream);
+// Sequences whose query columns one pass over a prefix tile serves.
+int q8_shared_block(int hq);
+
 cudaError_t launch_q8_decode_simt(const DecodeQ8Args& a, mqa_dtype_t dtype, cudaStream_t stream);
 int q8_simt_ctas_per_sm(int d_k, int d_v, int hq);
 int q8_simt_tile_rows();

@@ -135,7 +135,10 @@ mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, const ui
   if (workspace_bytes_given < workspace_bytes(b, g, hq, d_v)) return MQA_ERR_INVALID_ARG;
   if ((d_k != 32 && d_k != 64 && d_k != 128) || (d_v != 32 && d_v != 64 && d_v != 128)) return MQA_ERR_UNSUPPORTED;
   const bool simt_ok = int64_t(hq) * d_k <= 4096 && int64_t(hq) * d_v <= 4096;
-  if (path == MQA_PATH_TCGEN05 || !simt_ok) return MQA_ERR_UNSUPPORTED;
+  const bool tc_ok = dtype == MQA_BF16 && q8::q8_tc_supported(d_k, d_v, hq);
+  if (path == MQA_PATH_TCGEN05 ? !tc_ok : path == MQA_PATH_SIMT ? !simt_ok : !tc_ok && !simt_ok)
+    return MQA_ERR_UNSUPPORTED;
+  const bool use_tc = path == MQA_PATH_TCGEN05 || (path == MQA_PATH_AUTO && tc_ok);
 
   const int sms = sm_count();
   if (sms <= 0) return MQA_ERR_CUDA;
@@ -156,15 +159,75 @@ mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, const ui
   a.hq = hq;
   a.window = opts ? opts->window : 0;
   const int span_max = a.window > 0 && a.window < m_max ? a.window : m_max;
-  a.no_merge = span_max <= q8::q8_simt_tile_rows();
+  a.no_merge = span_max <= (use_tc ? q8::q8_tc_tile_rows(hq) : q8::q8_simt_tile_rows());
   a.scale = scale;
   a.ws = carve_workspace(workspace, b, g, hq);
   a.flags = status_flags;
-  const int grid = opts && opts->num_ctas > 0 ? opts->num_ctas : sms * q8::q8_simt_ctas_per_sm(d_k, d_v, hq);
+  const int grid = opts && opts->num_ctas > 0 ? opts->num_ctas : sms * (use_tc ? 1 : q8::q8_simt_ctas_per_sm(d_k, d_v, hq));
   a.grid = grid < 1 ? 1 : (grid > kMaxCtas ? kMaxCtas : grid);
-  if (q8::launch_q8_decode_simt(a, dtype, stream) != cudaSuccess) return MQA_ERR_CUDA;
+  const cudaError_t e = use_tc ? q8::launch_q8_decode_tc(a, stream) : q8::launch_q8_decode_simt(a, dtype, stream);
+  if (e == cudaErrorInvalidValue) return MQA_ERR_INVALID_ARG;   // sizes past the kernel's index range
+  if (e != cudaSuccess) return MQA_ERR_CUDA;
   if (!a.no_merge && launch_merge(merge_args(a), dtype, stream) != cudaSuccess) return MQA_ERR_CUDA;
   return MQA_OK;
+}
+
+size_t mqa_q8_decode_shared_workspace_size(int b, int h, int g, int d) {
+  if (b < 0 || h < 1 || g < 1 || h % g != 0 || d < 1 || h / g > 64) return 0;
+  const int spb = q8::q8_shared_block(h / g), nseq = (b + spb - 1) / spb + b;
+  return workspace_bytes(nseq, g, spb * (h / g), d);
+}
+
+mqa_status_t mqa_q8_decode_shared(void* o, const void* q, const void* prefix_k, const uint8_t* prefix_k_exps,
+                                  const void* prefix_v, const uint8_t* prefix_v_exps, const int32_t* prefix_len,
+                                  const void* k_codes, const uint8_t* k_exps, const void* v_codes,
+                                  const uint8_t* v_exps, const int32_t* lens, int b, int h, int g, int m_p, int m_s,
+                                  int d, float scale, mqa_dtype_t dtype, void* workspace, size_t workspace_bytes_given,
+                                  int32_t* status_flags, cudaStream_t stream) {
+  if (b < 0 || h < 1 || g < 1 || h % g != 0 || m_p < 1 || m_s < 1 || d < 1 || !valid_dtype(dtype) ||
+      !std::isfinite(scale))
+    return MQA_ERR_INVALID_ARG;
+  if (b == 0) return MQA_OK;
+  if (!all_aligned16({o, q, prefix_k, prefix_v, prefix_len, k_codes, v_codes, lens}) || !prefix_k_exps ||
+      !prefix_v_exps || !k_exps || !v_exps || !workspace || !aligned256(workspace))
+    return MQA_ERR_INVALID_ARG;
+  if (int64_t(b) * g > (int64_t(1) << 29) || int64_t(b) * m_s * g > (int64_t(1) << 40) ||
+      int64_t(m_p) * g > (int64_t(1) << 40) || int64_t(b) * h >= (int64_t(1) << 31))
+    return MQA_ERR_INVALID_ARG;
+  const int hq = h / g;
+  if (dtype != MQA_BF16 || !q8::q8_tc_supported(d, d, hq)) return MQA_ERR_UNSUPPORTED;
+  if (workspace_bytes_given < mqa_q8_decode_shared_workspace_size(b, h, g, d)) return MQA_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms <= 0) return MQA_ERR_CUDA;
+  q8::TcArgs a = {};
+  a.o = o;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.ke = k_exps;
+  a.ve = v_exps;
+  a.lens = lens;
+  a.pke = prefix_k_exps;
+  a.pve = prefix_v_exps;
+  a.plen = prefix_len;
+  a.b = b;
+  a.h = h;
+  a.g = g;
+  a.hq = hq;
+  a.m = m_s;
+  a.m_p = m_p;
+  a.spb = q8::q8_shared_block(hq);
+  a.nblk = (b + a.spb - 1) / a.spb;
+  a.nseq = a.nblk + b;
+  a.cols = a.spb * hq;
+  a.scale = scale;
+  a.ws = carve_workspace(workspace, a.nseq, g, a.cols);
+  a.flags = status_flags;
+  a.grid = sms;
+  const cudaError_t e = q8::launch_q8_decode_shared(a, static_cast<const uint8_t*>(prefix_k),
+                                                    static_cast<const uint8_t*>(prefix_v),
+                                                    static_cast<const uint8_t*>(k_codes),
+                                                    static_cast<const uint8_t*>(v_codes), stream);
+  if (e == cudaErrorInvalidValue) return MQA_ERR_INVALID_ARG;   // sizes past the kernel's index range
+  return e == cudaSuccess ? MQA_OK : MQA_ERR_CUDA;
 }
 
 }  // extern "C"

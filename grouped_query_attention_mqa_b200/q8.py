@@ -12,10 +12,12 @@ and K/V head, for keys and for values.  A row's values are
     q8.append(cache, k_new, v_new, pos)              # one row per sequence, or
     q8.append(cache, k_new, v_new, pos, cu_new=cu)   # packed rows, ragged counts
     o = q8.decode(q, cache, lens, scale)
+    o = q8.decode_shared(q, prefix, prefix_len, cache, lens, scale)   # prefix: a Cache of b = 1
     k, v = q8.read(cache, cu_rows, total)
 
-Every call has a plan (``AppendPlan``, ``ReadPlan``, ``DecodePlan``) that
-marshals its arguments once; ``run()`` is then one C call on those buffers.
+Every call has a plan (``AppendPlan``, ``ReadPlan``, ``DecodePlan``,
+``SharedPlan``) that marshals its arguments once; ``run()`` is then one C call
+on those buffers.
 """
 from __future__ import annotations
 
@@ -33,6 +35,8 @@ SIGNATURES = {
     "mqa_q8_decode_workspace_size": (_c_size, [_c_int] * 4),
     "mqa_q8_decode": (_c_int, [_c_ptr] * 7 + [_c_int] * 6 + [_c_float, _c_int, _c_ptr, _c_size, _c_ptr,
                                                              ctypes.POINTER(DecodeOptions), _c_ptr]),
+    "mqa_q8_decode_shared_workspace_size": (_c_size, [_c_int] * 4),
+    "mqa_q8_decode_shared": (_c_int, [_c_ptr] * 12 + [_c_int] * 6 + [_c_float, _c_int, _c_ptr, _c_size, _c_ptr, _c_ptr]),
 }
 
 _LIB = None
@@ -226,6 +230,39 @@ class DecodePlan(_Plan):
                    _ptr(status_flags), ctypes.byref(self._opts)), stream)
 
 
+class SharedPlan(_Plan):
+    """mqa_q8_decode_shared: o [b, h, d] of q [b, h, d], every sequence over
+    the first prefix_len[0] rows of ``prefix`` (a Cache of one sequence;
+    prefix_len int32 [1]) and then its own first lens[b] rows of ``cache``.
+    ``run()`` returns o."""
+
+    def __init__(self, q, prefix, prefix_len, cache, lens, scale, out=None, workspace=None, status_flags=None,
+                 stream=None):
+        import torch
+        prefix, cache = Cache(*prefix), Cache(*cache)
+        b, m_s, g, d, d_v = _cache_shape(cache, "decode_shared")
+        one, m_p, *rest = _cache_shape(prefix, "decode_shared")
+        if one != 1 or rest != [g, d, d_v] or d != d_v:
+            raise ValueError("decode_shared: the prefix must be one sequence of the caches' g and d")
+        _check_cuda(q, prefix_len, lens, out, workspace, status_flags)
+        _same_device(cache.k, *prefix, *cache[1:], q, prefix_len, lens, out, workspace, status_flags)
+        if q.dim() != 3 or q.shape[0] != b or q.shape[2] != d:
+            raise ValueError("decode_shared: q must be [b, h, d] of the cache's b and d")
+        h = q.shape[1]
+        _check_i32(prefix_len, 1, "prefix_len")
+        _check_i32(lens, b, "lens")
+        if out is None:
+            out = torch.empty((b, h, d), dtype=q.dtype, device=q.device)
+        elif tuple(out.shape) != (b, h, d) or out.dtype != q.dtype:
+            raise ValueError("decode_shared: out must be [b, h, d] in q's dtype")
+        ws = _workspace(workspace, int(lib().mqa_q8_decode_shared_workspace_size(b, h, g, d)), q.device)
+        self.out = out
+        self._set("mqa_q8_decode_shared", out, (q, *prefix, prefix_len, *cache, lens, out, ws, status_flags),
+                  tuple(_ptr(t) for t in (out, q, *prefix, prefix_len, *cache, lens)) +
+                  (b, h, g, m_p, m_s, d, float(scale), _dtype_code(q), _ptr(ws), ws.numel() * ws.element_size(),
+                   _ptr(status_flags)), stream)
+
+
 def append(cache, k_new, v_new, pos, cu_new=None, status_flags=None, stream=None):
     """Quantise new rows into the cache, in place (see ``AppendPlan``)."""
     return AppendPlan(cache, k_new, v_new, pos, cu_new, status_flags, stream).run()
@@ -240,3 +277,8 @@ def decode(q, cache, lens, scale, out=None, workspace=None, status_flags=None, p
            stream=None):
     """One decode step's attention over the cache (see ``DecodePlan``)."""
     return DecodePlan(q, cache, lens, scale, out, workspace, status_flags, path, num_ctas, window, stream).run()
+
+
+def decode_shared(q, prefix, prefix_len, cache, lens, scale, out=None, workspace=None, status_flags=None, stream=None):
+    """One decode step of a batch behind one shared prefix (see ``SharedPlan``)."""
+    return SharedPlan(q, prefix, prefix_len, cache, lens, scale, out, workspace, status_flags, stream).run()

@@ -1,6 +1,7 @@
 /*
  * libmqa, 8-bit K/V caches: the cache's rows quantised as they are written,
- * read back, and attended to by single-token queries.
+ * read back, and attended to by single-token queries — each sequence over its
+ * own rows, or a whole batch behind one shared prefix.
  *
  * The attention is that of mqa.h (mqa_decode): the velog paper review of
  * "Fast Transformer Decoding", §3 MultiquerySelfAttentionIncremental, with the
@@ -15,7 +16,8 @@
  *                                              are NaN; largest 448)
  *   exponents  device uint8 [b, g, m_max]
  *
- * The library writes E in [1, 254].  A power of two costs e4m3 no precision
+ * The library writes E in [1, 254]; rows that are attended to must not hold
+ * E = 255.  A power of two costs e4m3 no precision
  * (it is a floating format), makes code * s exact in bf16 and fp32, and makes
  * quantising what was read back give the same codes and exponent again.  The
  * exponents of one head lie in row order, so a tile's are one short run.
@@ -98,8 +100,9 @@ MQA_API mqa_status_t mqa_q8_read(void* k_out, void* v_out, const void* k_codes, 
  *
  * Rows at or past lens[b], and rows before the window, never count, whatever
  * codes and exponents they hold.  Statistics and sums are fp32.
- * The CUDA-core path takes both types with d_k, d_v in {32, 64, 128} and
- * h/g * d_k, h/g * d_v <= 4096.
+ * Paths: the tensor-core path takes bf16 with d_k = d_v = 128 and h/g <= 64,
+ * and is then the automatic choice; the CUDA-core path takes both types with
+ * d_k, d_v in {32, 64, 128} and h/g * d_k, h/g * d_v <= 4096.
  * MQA_ERR_UNSUPPORTED for other shapes.  q holding an infinity or NaN gives a
  * NaN output for that head.
  */
@@ -109,6 +112,37 @@ MQA_API mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, 
                                    int m_max, int d_k, int d_v, float scale, mqa_dtype_t dtype, void* workspace,
                                    size_t workspace_bytes, int32_t* status_flags, const mqa_decode_opts_t* opts,
                                    cudaStream_t stream);
+
+/*
+ * mqa_q8_decode_shared — one decode step of a batch whose sequences all begin
+ * with the same prefix, cached once.
+ *
+ * Sequence s attends over the prefix rows 0 .. prefix_len[0]-1, then over its
+ * own rows 0 .. lens[s]-1.  The prefix is read for the whole batch, many
+ * sequences' queries per pass over a tile; the two parts of each output are
+ * joined by their log-sum-exps, which is exact.  (mqa_decode_beam shares a
+ * prefix between the beams of one sequence, over a bf16 cache.)
+ *
+ *   o, q              device [b, h, d]  (bf16)
+ *   prefix_k/v codes  device [m_p, g, d], exponents [g, m_p]
+ *   prefix_len        device int32 [1]  (clamped to [0, m_p])
+ *   k/v codes         device [b, m_s, g, d], exponents [b, g, m_s]
+ *   lens              device int32 [b]  (clamped to [0, m_s])
+ *   workspace         device, mqa_q8_decode_shared_workspace_size(b, h, g, d)
+ *                     bytes, as for mqa_q8_decode
+ *
+ * MQA_FLAG_LEN_CLAMPED reports lengths outside [0, m]; 0 is a length here.
+ * A sequence with no rows at all gets a zero row.  Built for bf16, d = 128
+ * and h/g <= 64 (MQA_ERR_UNSUPPORTED otherwise).
+ */
+MQA_API size_t mqa_q8_decode_shared_workspace_size(int b, int h, int g, int d);
+MQA_API mqa_status_t mqa_q8_decode_shared(void* o, const void* q, const void* prefix_k, const uint8_t* prefix_k_exps,
+                                          const void* prefix_v, const uint8_t* prefix_v_exps,
+                                          const int32_t* prefix_len, const void* k_codes, const uint8_t* k_exps,
+                                          const void* v_codes, const uint8_t* v_exps, const int32_t* lens, int b,
+                                          int h, int g, int m_p, int m_s, int d, float scale, mqa_dtype_t dtype,
+                                          void* workspace, size_t workspace_bytes, int32_t* status_flags,
+                                          cudaStream_t stream);
 
 #ifdef __cplusplus
 }

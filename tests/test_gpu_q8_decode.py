@@ -59,13 +59,75 @@ def test_simt(case, dtype):
         run(np.random.default_rng(sum(lens) + ctas), lens, h, g, m_max, d_k, d_v, dtype, "simt", ctas=ctas)
 
 
-@pytest.mark.parametrize("path,dtype,d", [("simt", "f32", 64), ("simt", "bf16", 32)])
+TC = [  # lens, h, g, m_max: tile edges (128 and 256 rows), all group widths, split and whole segments
+    ([1], 1, 1, 1),
+    ([1, 127, 128, 129, 255, 256, 257], 8, 1, 260),
+    ([700, 511, 512, 513], 32, 1, 700),
+    ([300, 1, 256], 48, 3, 300),
+    ([640, 129, 1000], 64, 1, 1000),
+    ([385, 128, 2], 66, 2, 400),
+    ([400, 30], 40, 8, 400),
+    ([260, 90, 33], 24, 2, 260),
+    ([5] * 200 + [600] + [0] * 7 + [128] * 200, 16, 2, 600),     # more sequences than threads of the schedule
+]
+
+
+@pytest.mark.parametrize("case", TC, ids=lambda c: f"b{len(c[0])}h{c[1]}g{c[2]}m{c[3]}")
+def test_tensor_cores(case):
+    lens, h, g, m_max = case
+    for ctas in (0, 1, 5):
+        run(np.random.default_rng(sum(lens) + ctas), lens, h, g, m_max, 128, 128, "bf16", "tcgen05", ctas=ctas,
+            flag=binding.MQA_FLAG_LEN_CLAMPED if 0 in lens else 0)
+
+
+def test_tensor_cores_growing_logits():
+    """References that have to move, tile after tile: keys (and values) that
+    grow along the sequence."""
+    rng = np.random.default_rng(21)
+    for h in (16, 32, 64):
+        arrays = host_cache(rng, 2, 1500, 1, 128)
+        for i in (1, 3):
+            arrays[i] = (arrays[i] + (np.arange(1500) // 200)[None, None]).astype(np.uint8)
+        run(rng, [1500, 1111], h, 1, 1500, 128, 128, "bf16", "tcgen05", arrays=arrays, scale=0.02)
+        arrays[3] = arrays[3][:, :, ::-1].copy()
+        run(rng, [1500, 1111], h, 1, 1500, 128, 128, "bf16", "tcgen05", arrays=arrays, scale=0.02, ctas=1)
+
+
+def test_tensor_cores_attention_sink():
+    """A heavy row with small values: the others keep their precision."""
+    rng = np.random.default_rng(22)
+    arrays = host_cache(rng, 1, 4000, 1, 128, spread=0.2)
+    q, q64 = round_to(rng.standard_normal((1, 8, 128)), "bf16")
+    from oracle import q8_oracle
+    k0 = np.ones(128) * 3
+    q64[...] = np.abs(q64)
+    q = torch.from_numpy(q64).to(torch.bfloat16)
+    arrays[0][0, 0, 0], arrays[1][0, 0, 0] = q8_oracle.quantise(k0)
+    arrays[3][0, 0, 0] -= 7
+    o = q8.decode(q.cuda(), dev_cache(arrays), i32([4000]), 0.04)
+    ref, tol = attention(q64, cache_parts(arrays, [4000]), 1, 0.04, "bf16", two_terms=True)
+    assert_within(o, ref, tol, "sink")
+
+
+def test_queries_of_very_different_size():
+    """Each query row has a scale of its own; zeros, tiny and huge rows."""
+    rng = np.random.default_rng(23)
+    arrays = host_cache(rng, 2, 300, 1, 128)
+    size = np.exp2(rng.integers(-60, 3, (2, 16, 1)).astype(float))
+    size[0, 0] = 0
+    q, q64 = round_to(rng.standard_normal((2, 16, 128)) * size, "bf16")
+    o = q8.decode(q.cuda(), dev_cache(arrays), i32([300, 200]), 0.3, path="tcgen05")
+    ref, tol = attention(q64, cache_parts(arrays, [300, 200]), 1, 0.3, "bf16", two_terms=True)
+    assert_within(o, ref, tol)
+
+
+@pytest.mark.parametrize("path,dtype,d", [("simt", "f32", 64), ("simt", "bf16", 32), ("tcgen05", "bf16", 128)])
 @pytest.mark.parametrize("window", [1, 63, 64, 100, 1000])
 def test_window(path, dtype, d, window):
     run(np.random.default_rng(window), [1, 64, 65, 300, 299], 8, 2, 300, d, d, dtype, path, window=window)
 
 
-@pytest.mark.parametrize("path,dtype", [("simt", "f32"), ("simt", "bf16")])
+@pytest.mark.parametrize("path,dtype", [("simt", "f32"), ("simt", "bf16"), ("tcgen05", "bf16")])
 def test_empty_and_clamped_lengths(path, dtype):
     for m_max in (40, 300):   # without and with a merge
         rng = np.random.default_rng(m_max)
@@ -74,7 +136,7 @@ def test_empty_and_clamped_lengths(path, dtype):
             flag=binding.MQA_FLAG_LEN_CLAMPED)
 
 
-@pytest.mark.parametrize("path,dtype", [("simt", "f32"), ("simt", "bf16")])
+@pytest.mark.parametrize("path,dtype", [("simt", "f32"), ("simt", "bf16"), ("tcgen05", "bf16")])
 def test_sharp_and_flat_softmax(path, dtype):
     """Logits of one row far above the others, and all equal; value rows of
     very different magnitude, and rows of zeros."""
@@ -96,11 +158,17 @@ def test_nan_inputs_show():
     arrays = host_cache(rng, 2, 100, 2, 128)
     arrays[0][0, 50, 0, 3] = 0x7F
     q, _ = round_to(rng.standard_normal((2, 8, 128)), "bf16")
-    for path in ("simt",):
+    for path in ("simt", "tcgen05"):
         o = q8.decode(q.cuda(), dev_cache(arrays), i32([100, 100]), 0.1, path=path)
         nan = torch.isnan(o).all(-1).cpu().numpy()
         some = torch.isnan(o).any(-1).cpu().numpy()
         assert nan[0, :4].all() and not some[0, 4:].any() and not some[1].any()
+        bad = q.clone()
+        bad[1, 5, 100], bad[0, 6, 0] = float("inf"), float("nan")
+        arrays2 = host_cache(np.random.default_rng(5), 2, 100, 2, 128)
+        o = q8.decode(bad.cuda(), dev_cache(arrays2), i32([100, 100]), 0.1, path=path)
+        some = torch.isnan(o).any(-1).cpu()
+        assert bool(torch.isnan(o[1, 5]).all()) and bool(torch.isnan(o[0, 6]).all()) and int(some.sum()) == 2
 
 
 def test_append_then_decode_steps():
@@ -144,3 +212,32 @@ def test_same_call_twice_is_the_same():
     cache, lens = dev_cache(arrays), i32([900, 1, 511])
     a = q8.decode(q.cuda(), cache, lens, 0.2).clone()
     assert torch.equal(a, q8.decode(q.cuda(), cache, lens, 0.2))
+
+
+def test_two_captured_calls_do_not_share_a_workspace():
+    """Two plans captured into graphs and replayed in turn on two streams."""
+    rng = np.random.default_rng(14)
+    plans, want = [], []
+    for k in range(2):
+        arrays = host_cache(rng, 4, 2000, 2, 128)
+        lens = [2000, 1500, 3, 900]
+        q, q64 = round_to(rng.standard_normal((4, 32, 128)), "bf16")
+        plans.append(q8.DecodePlan(q.cuda(), dev_cache(arrays), i32(lens), 0.1))
+        want.append(attention(q64, cache_parts(arrays, lens), 2, 0.1, "bf16", two_terms=True))
+    torch.cuda.synchronize()
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for p in plans:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            p.run()
+        graphs.append(g)
+    for p in plans:
+        p.out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for p, (ref, tol) in zip(plans, want):
+        assert_within(p.out, ref, tol)

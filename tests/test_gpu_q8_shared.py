@@ -1,0 +1,141 @@
+"""mqa_q8_decode_shared against attention in float64 over the prefix's rows
+followed by each sequence's own, with tolerances derived from the arithmetic
+(``q8_util``)."""
+import numpy as np
+import pytest
+import torch
+
+from grouped_query_attention_mqa_b200 import binding, q8
+from grouped_query_attention_mqa_b200.build import build
+
+from q8_util import assert_within, attention, cache_parts, dev_cache, host_cache, round_to, rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build()
+    q8.lib()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def parts_of(prefix, p_len, arrays, lens):
+    p = cache_parts(prefix, [p_len])[0]
+    return [p + own for own in cache_parts(arrays, lens)]
+
+
+def run(rng, lens, h, g, m_p, p_len, m_s, scale=0.09, prefix=None, arrays=None, flag=0, q_spread=0.0):
+    b = len(lens)
+    prefix = host_cache(rng, 1, m_p, g, 128, lens=[p_len]) if prefix is None else prefix
+    arrays = host_cache(rng, b, m_s, g, 128, lens=lens) if arrays is None else arrays
+    q, q64 = round_to(rows(rng, (b, h, 128), q_spread), "bf16")
+    flags = i32([0])
+    o = q8.decode_shared(q.cuda(), dev_cache(prefix), i32([p_len]), dev_cache(arrays), i32(lens), scale, status_flags=flags)
+    torch.cuda.synchronize()
+    assert int(flags) == flag
+    ref, tol = attention(q64, parts_of(prefix, p_len, arrays, lens), g, scale, "bf16", two_terms=True)
+    assert_within(o, ref, tol, f"b{b} h{h} g{g} p{p_len}")
+
+
+CASES = [  # lens, h, g, m_p, p_len, m_s
+    ([1], 1, 1, 1, 1, 1),
+    ([3, 0, 1], 8, 1, 200, 130, 5),
+    ([5, 128, 129, 0, 1, 77, 300, 2, 9], 16, 2, 513, 512, 300),
+    ([10, 20], 64, 1, 300, 257, 20),
+    ([7] * 13, 24, 2, 150, 150, 9),                  # 12 heads per group: five sequences per block
+    ([1, 2, 3], 34, 1, 129, 128, 4),                 # 34 heads: one sequence per block
+    ([40, 130, 260], 12, 12, 400, 399, 260),         # one head per group: 64 sequences per block
+    ([4] * 130, 4, 1, 700, 650, 4),
+    ([0] * 5, 8, 2, 100, 99, 3),                     # nothing but the prefix
+    ([2] * 250 + [30], 8, 1, 128, 100, 30),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"b{len(c[0])}h{c[1]}g{c[2]}p{c[4]}")
+def test_shared(case):
+    lens, h, g, m_p, p_len, m_s = case
+    run(np.random.default_rng(sum(lens) + m_p), lens, h, g, m_p, p_len, m_s)
+
+
+def test_no_prefix_and_no_rows():
+    rng = np.random.default_rng(1)
+    run(rng, [5, 0, 130], 8, 2, 64, 0, 130)           # the empty sequence's row is zero
+    run(rng, [0, 0], 8, 2, 64, 0, 4)
+
+
+def test_lengths_outside_the_caches_are_clamped():
+    rng = np.random.default_rng(2)
+    prefix, arrays = host_cache(rng, 1, 50, 1, 128), host_cache(rng, 3, 6, 1, 128)
+    for p_len, lens in ((51, [1, 2, 3]), (-4, [6, 2, 0]), (9, [7, -1, 0])):
+        run(rng, lens, 8, 1, 50, p_len, 6, prefix=prefix, arrays=arrays, flag=binding.MQA_FLAG_LEN_CLAMPED)
+
+
+def test_prefix_or_own_rows_dominate():
+    """Logits far apart between the two parts, in either direction, and value
+    rows of different size."""
+    rng = np.random.default_rng(3)
+    for up in (0, 1):
+        prefix, arrays = host_cache(rng, 1, 700, 2, 128), host_cache(rng, 6, 200, 2, 128)
+        (arrays if up else prefix)[1][...] += 4
+        (prefix if up else arrays)[3][...] += 9
+        run(rng, [200, 1, 130, 199, 0, 60], 16, 2, 700, 690, 200, prefix=prefix, arrays=arrays, scale=0.2)
+
+
+def test_matches_decode_over_joined_rows():
+    """The same rows as one cache through mqa_q8_decode: both within the sum of
+    two tolerances of each other (each is within one of the exact output)."""
+    rng = np.random.default_rng(4)
+    b, g, h, P, m = 5, 2, 16, 300, 40
+    lens = [40, 1, 0, 17, 33]
+    prefix, arrays = host_cache(rng, 1, P, g, 128), host_cache(rng, b, m, g, 128)
+    joined = [np.concatenate([np.repeat(p, b, 0), a], axis=1 if p.ndim == 4 else 2) for p, a in zip(prefix, arrays)]
+    q, q64 = round_to(rng.standard_normal((b, h, 128)), "bf16")
+    o1 = q8.decode_shared(q.cuda(), dev_cache(prefix), i32([P]), dev_cache(arrays), i32(lens), 0.1)
+    o2 = q8.decode(q.cuda(), dev_cache(joined), i32([P + n for n in lens]), 0.1)
+    _, tol = attention(q64, parts_of(prefix, P, arrays, lens), g, 0.1, "bf16", two_terms=True)
+    assert (np.abs((o1.double() - o2.double()).cpu().numpy()) <= 2 * tol).all()
+
+
+def test_steps_behind_a_shared_prompt():
+    """A served batch: one prompt quantised once, then steps that append each
+    sequence's row and attend, captured and replayed."""
+    from oracle import q8_oracle
+    rng = np.random.default_rng(5)
+    b, h, g, P, m = 6, 16, 2, 333, 12
+    prefix, cache = q8.new_cache(1, 400, g, 128), q8.new_cache(b, m, g, 128)
+    pk, pk64 = round_to(rows(rng, (P, g, 128)), "bf16")
+    pv, pv64 = round_to(rows(rng, (P, g, 128)), "bf16")
+    q8.append(prefix, pk.cuda(), pv.cuda(), i32([0]), cu_new=i32([0, P]))
+    host_prefix = []
+    for x in (pk64, pv64):
+        c, e = q8_oracle.quantise(x)
+        host_prefix += [c[None], np.ascontiguousarray(e.T)[None]]
+    kn, vn = (torch.zeros((b, g, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qd = torch.zeros((b, h, 128), dtype=torch.bfloat16, device="cuda")
+    pos, lens, p_len = i32([0] * b), i32([1] * b), i32([P])
+    step = (q8.AppendPlan(cache, kn, vn, pos), q8.SharedPlan(qd, prefix, p_len, cache, lens, 0.09))
+    arrays = [np.zeros((b, m, g, 128), np.uint8), np.zeros((b, g, m), np.uint8)]
+    arrays = arrays + [x.copy() for x in arrays]
+    graph = None
+    for t in range(m):
+        k, k64 = round_to(rows(rng, (b, g, 128)), "bf16")
+        v, v64 = round_to(rows(rng, (b, g, 128)), "bf16")
+        q, q64 = round_to(rng.standard_normal((b, h, 128)), "bf16")
+        kn.copy_(k), vn.copy_(v), qd.copy_(q), pos.fill_(t), lens.fill_(t + 1)
+        if t == 2:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step[0].run(), step[1].run()
+        if graph is None:
+            step[0].run(), step[1].run()
+        else:
+            graph.replay()
+        for i, x in enumerate((k64, v64)):
+            c, e = q8_oracle.quantise(x)
+            arrays[2 * i][:, t], arrays[2 * i + 1][:, :, t] = c, e
+        ref, tol = attention(q64, parts_of(host_prefix, P, arrays, [t + 1] * b), g, 0.09, "bf16", two_terms=True)
+        assert_within(step[1].out, ref, tol, f"step {t}")

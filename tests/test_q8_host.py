@@ -148,6 +148,29 @@ def test_decode_refusals(lib):
     assert size(2, 8, 3, 128) == 0 and size(-1, 8, 1, 128) == 0 and size(0, 8, 1, 128) > 0
 
 
+def _shared(lib, **kw):
+    a = dict(o=FAKE, q=FAKE, pk=FAKE, pke=FAKE, pv=FAKE, pve=FAKE, pl=FAKE, k=FAKE, ke=FAKE, v=FAKE, ve=FAKE, lens=FAKE,
+             b=2, h=8, g=1, m_p=64, m_s=16, d=128, scale=1.0, dtype=binding.MQA_BF16, ws=FAKE, ws_bytes=1 << 40)
+    a.update(kw)
+    return lib.mqa_q8_decode_shared(a["o"], a["q"], a["pk"], a["pke"], a["pv"], a["pve"], a["pl"], a["k"], a["ke"],
+                                    a["v"], a["ve"], a["lens"], a["b"], a["h"], a["g"], a["m_p"], a["m_s"], a["d"],
+                                    a["scale"], a["dtype"], a["ws"], a["ws_bytes"], None, None)
+
+
+def test_shared_refusals(lib):
+    for name in ("o", "q", "pk", "pke", "pv", "pve", "pl", "k", "ke", "v", "ve", "lens", "ws"):
+        assert _shared(lib, **{name: None}) == INV
+    for name in ("o", "q", "pk", "pv", "pl", "k", "v", "lens", "ws"):
+        assert _shared(lib, **{name: ODD}) == INV
+    size = lib.mqa_q8_decode_shared_workspace_size
+    assert _shared(lib, ws_bytes=size(2, 8, 1, 128) - 1) == INV
+    assert _shared(lib, g=3) == INV and _shared(lib, m_p=0) == INV and _shared(lib, m_s=0) == INV and _shared(lib, b=-1) == INV
+    assert _shared(lib, scale=float("inf")) == INV and _shared(lib, dtype=9) == INV
+    assert _shared(lib, dtype=binding.MQA_F32) == UNS and _shared(lib, d=64) == UNS and _shared(lib, h=65) == UNS
+    assert _shared(lib, b=0) == OK
+    assert size(2, 8, 3, 128) == 0 and size(2, 65, 1, 128) == 0 and size(0, 8, 1, 128) > 0
+
+
 def test_binding_refuses_other_layouts():
     with pytest.raises(ValueError, match="contiguous CUDA"):
         q8.AppendPlan(q8.new_cache(1, 4, 1, 16, device="cpu"), None, None, None)
