@@ -71,37 +71,66 @@ cudaError_t launch_q8_read(void* k_out, void* v_out, const uint8_t* k, const uin
                            const uint8_t* ve, const int32_t* start, const int32_t* cu, int b, int total, int m_max,
                            int g, int d_k, int d_v, mqa_dtype_t dtype, int32_t* flags, cudaStream_t stream);
 
-// The tensor-core kernel's view of a batch: `nseq` row lists ("sequences"),
-// each of g segments (one per K/V head) with up to `cols` query columns.
-// A plain decode: one list per sequence.  A shared prefix: first `nblk` lists
-// that are the prefix, each for `spb` sequences' queries, then one list per
-// sequence for its own rows.
+// Attention on the tensor cores (bf16, head size 128).
 struct TcArgs {
   void* o;
   const __nv_bfloat16* q;
   const uint8_t* ke;     // exponents [b, g, m]
   const uint8_t* ve;
   const int32_t* lens;   // [b]
-  const uint8_t* pke;    // prefix exponents [g, m_p]
-  const uint8_t* pve;
-  const int32_t* plen;   // [1]
-  int b, h, g, hq, m, m_p;
-  int window, no_merge;
-  int nseq, nblk, spb, cols;
+  int b, h, g, hq, m;
+  int window;            // 0: all rows
+  int no_merge;          // no segment spans two tiles: every output row is written by the decode itself
+  int partials;          // every segment leaves a partial, whole ones too (another part joins them)
+  int groups;            // groups of g CTAs, one per K/V head
   float scale;
   Workspace ws;
   int32_t* flags;
-  int grid;
 };
 
-bool q8_tc_supported(int d_k, int d_v, int hq);
-int q8_tc_tile_rows(int hq);
-cudaError_t launch_q8_decode_tc(const DecodeQ8Args& a, cudaStream_t stream);
-// Prefix and own rows of a whole batch, and the merge.
-cudaError_t launch_q8_decode_shared(const TcArgs& a, const uint8_t* pk, const uint8_t* pv, const uint8_t* k,
-                                    const uint8_t* v, cudaStream_t stream);
-// Sequences whose query columns one pass over a prefix tile serves.
-int q8_shared_block(int hq);
+// Where group `group` leaves its partial of sequence `seq` and K/V head `head`:
+// consecutive sequences' groups meet in one group at most, so group + seq is
+// theirs alone.  Fewer than (groups + b) g slots.
+__device__ __forceinline__ int64_t tc_slot(int group, int seq, int g, int head) {
+  return (int64_t(group) + seq) * g + head;
+}
+
+// Groups of CTAs for a wish of `ctas` (at least one group).
+inline int tc_groups(int ctas, int g) {
+  const int n = ctas / g;
+  return n < 1 ? 1 : n;
+}
+
+bool q8_tc_supported(int d_k, int d_v, int hq, int g);
+bool q8_tc_fits(int b, int m);
+int q8_tc_tile_rows();
+int q8_tc_ctas_per_sm();
+cudaError_t launch_q8_decode_tc(const TcArgs& a, const uint8_t* k, const uint8_t* v, cudaStream_t stream);
+
+// A prefix that all sequences share: every query row against it, in blocks of
+// kPrefixRows rows of one K/V head.  Leaves a partial per (CTA, block).
+constexpr int kPrefixRows = 128, kPrefixKeys = 64;   // query rows of a block, keys of a tile
+constexpr int kPrefixMaxCtas = 512;
+__device__ __forceinline__ int prefix_tiles(int len) { return (len + kPrefixKeys - 1) / kPrefixKeys; }
+// CTAs that share `total` tiles.
+__device__ __forceinline__ int prefix_ctas(int64_t total, int grid) { return int(total < grid ? total : int64_t(grid)); }
+struct PrefixArgs {
+  const __nv_bfloat16* q;
+  const uint8_t* ke;     // exponents [g, m_p]
+  const uint8_t* ve;
+  const int32_t* len;    // [1]
+  int b, h, g, hq, m_p;
+  int blocks;            // blocks of query rows per K/V head
+  float scale;
+  float* part_o;         // [slots][kPrefixRows][d], slot = CTA + head * blocks + block
+  float* part_lse;       // [slots][kPrefixRows]
+  int32_t* flags;
+  int grid;
+};
+cudaError_t launch_q8_prefix(const PrefixArgs& a, const uint8_t* k, const uint8_t* v, cudaStream_t stream);
+
+// Joins the partials of the own rows (and of a prefix, if given).
+cudaError_t launch_q8_merge(const TcArgs& a, const PrefixArgs* prefix, cudaStream_t stream);
 
 cudaError_t launch_q8_decode_simt(const DecodeQ8Args& a, mqa_dtype_t dtype, cudaStream_t stream);
 int q8_simt_ctas_per_sm(int d_k, int d_v, int hq);

@@ -135,13 +135,43 @@ mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, const ui
   if (workspace_bytes_given < workspace_bytes(b, g, hq, d_v)) return MQA_ERR_INVALID_ARG;
   if ((d_k != 32 && d_k != 64 && d_k != 128) || (d_v != 32 && d_v != 64 && d_v != 128)) return MQA_ERR_UNSUPPORTED;
   const bool simt_ok = int64_t(hq) * d_k <= 4096 && int64_t(hq) * d_v <= 4096;
-  const bool tc_ok = dtype == MQA_BF16 && q8::q8_tc_supported(d_k, d_v, hq);
+  const bool tc_ok = dtype == MQA_BF16 && q8::q8_tc_supported(d_k, d_v, hq, g);
   if (path == MQA_PATH_TCGEN05 ? !tc_ok : path == MQA_PATH_SIMT ? !simt_ok : !tc_ok && !simt_ok)
     return MQA_ERR_UNSUPPORTED;
   const bool use_tc = path == MQA_PATH_TCGEN05 || (path == MQA_PATH_AUTO && tc_ok);
 
   const int sms = sm_count();
   if (sms <= 0) return MQA_ERR_CUDA;
+  const int window = opts ? opts->window : 0;
+  const int span_max = window > 0 && window < m_max ? window : m_max;
+  const Workspace ws = carve_workspace(workspace, b, g, hq);
+  const int wish = opts && opts->num_ctas > 0 ? opts->num_ctas
+                                              : sms * (use_tc ? q8::q8_tc_ctas_per_sm() : q8::q8_simt_ctas_per_sm(d_k, d_v, hq));
+  const int grid = wish < 1 ? 1 : (wish > kMaxCtas ? kMaxCtas : wish);
+  if (use_tc) {
+    q8::TcArgs a = {};
+    a.o = o;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.ke = k_exps;
+    a.ve = v_exps;
+    a.lens = lens;
+    a.b = b;
+    a.h = h;
+    a.g = g;
+    a.hq = hq;
+    a.m = m_max;
+    a.window = window;
+    a.no_merge = span_max <= q8::q8_tc_tile_rows();   // no segment can be split: every row is final as it is
+    a.groups = q8::tc_groups(grid, g);
+    a.scale = scale;
+    a.ws = ws;
+    a.flags = status_flags;
+    if (!q8::q8_tc_fits(b, m_max)) return MQA_ERR_INVALID_ARG;   // sizes past the kernel's index range
+    if (q8::launch_q8_decode_tc(a, static_cast<const uint8_t*>(k_codes), static_cast<const uint8_t*>(v_codes), stream) !=
+            cudaSuccess ||
+        (!a.no_merge && q8::launch_q8_merge(a, nullptr, stream) != cudaSuccess)) return MQA_ERR_CUDA;
+    return MQA_OK;
+  }
   q8::DecodeQ8Args a;
   a.o = o;
   a.q = q;
@@ -157,25 +187,37 @@ mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, const ui
   a.d_k = d_k;
   a.d_v = d_v;
   a.hq = hq;
-  a.window = opts ? opts->window : 0;
-  const int span_max = a.window > 0 && a.window < m_max ? a.window : m_max;
-  a.no_merge = span_max <= (use_tc ? q8::q8_tc_tile_rows(hq) : q8::q8_simt_tile_rows());
+  a.window = window;
+  a.no_merge = span_max <= q8::q8_simt_tile_rows();
   a.scale = scale;
-  a.ws = carve_workspace(workspace, b, g, hq);
+  a.ws = ws;
   a.flags = status_flags;
-  const int grid = opts && opts->num_ctas > 0 ? opts->num_ctas : sms * (use_tc ? 1 : q8::q8_simt_ctas_per_sm(d_k, d_v, hq));
-  a.grid = grid < 1 ? 1 : (grid > kMaxCtas ? kMaxCtas : grid);
-  const cudaError_t e = use_tc ? q8::launch_q8_decode_tc(a, stream) : q8::launch_q8_decode_simt(a, dtype, stream);
-  if (e == cudaErrorInvalidValue) return MQA_ERR_INVALID_ARG;   // sizes past the kernel's index range
-  if (e != cudaSuccess) return MQA_ERR_CUDA;
+  a.grid = grid;
+  if (q8::launch_q8_decode_simt(a, dtype, stream) != cudaSuccess) return MQA_ERR_CUDA;
   if (!a.no_merge && launch_merge(merge_args(a), dtype, stream) != cudaSuccess) return MQA_ERR_CUDA;
   return MQA_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// Workspace of a decode behind a shared prefix: the own rows' partials as for
+// a decode, then the prefix's.
+int64_t prefix_blocks(int b, int hq) { return (int64_t(b) * hq + q8::kPrefixRows - 1) / q8::kPrefixRows; }
+int64_t prefix_slots(int b, int g, int hq) { return q8::kPrefixMaxCtas + prefix_blocks(b, hq) * g; }
+size_t shared_bytes(int b, int g, int hq, int d) {
+  return workspace_bytes(b, g, hq, d) + align256(sizeof(float) * size_t(prefix_slots(b, g, hq)) * q8::kPrefixRows) +
+         sizeof(float) * size_t(prefix_slots(b, g, hq)) * q8::kPrefixRows * size_t(d);
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t mqa_q8_decode_shared_workspace_size(int b, int h, int g, int d) {
   if (b < 0 || h < 1 || g < 1 || h % g != 0 || d < 1 || h / g > 64) return 0;
-  const int spb = q8::q8_shared_block(h / g), nseq = (b + spb - 1) / spb + b;
-  return workspace_bytes(nseq, g, spb * (h / g), d);
+  return shared_bytes(b, g, h / g, d);
 }
 
 mqa_status_t mqa_q8_decode_shared(void* o, const void* q, const void* prefix_k, const uint8_t* prefix_k_exps,
@@ -192,41 +234,51 @@ mqa_status_t mqa_q8_decode_shared(void* o, const void* q, const void* prefix_k, 
       !prefix_v_exps || !k_exps || !v_exps || !workspace || !aligned256(workspace))
     return MQA_ERR_INVALID_ARG;
   if (int64_t(b) * g > (int64_t(1) << 29) || int64_t(b) * m_s * g > (int64_t(1) << 40) ||
-      int64_t(m_p) * g > (int64_t(1) << 40) || int64_t(b) * h >= (int64_t(1) << 31))
+      int64_t(m_p) * g > (int64_t(1) << 40) || int64_t(b) * h >= (int64_t(1) << 31) || !q8::q8_tc_fits(b, m_s) ||
+      !q8::q8_tc_fits(1, m_p))
     return MQA_ERR_INVALID_ARG;
   const int hq = h / g;
-  if (dtype != MQA_BF16 || !q8::q8_tc_supported(d, d, hq)) return MQA_ERR_UNSUPPORTED;
+  if (dtype != MQA_BF16 || !q8::q8_tc_supported(d, d, hq, g)) return MQA_ERR_UNSUPPORTED;
   if (workspace_bytes_given < mqa_q8_decode_shared_workspace_size(b, h, g, d)) return MQA_ERR_INVALID_ARG;
   const int sms = sm_count();
   if (sms <= 0) return MQA_ERR_CUDA;
+  q8::PrefixArgs p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.ke = prefix_k_exps;
+  p.ve = prefix_v_exps;
+  p.len = prefix_len;
+  p.b = b;
+  p.h = h;
+  p.g = g;
+  p.hq = hq;
+  p.m_p = m_p;
+  p.blocks = int(prefix_blocks(b, hq));
+  p.scale = scale;
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + workspace_bytes(b, g, hq, d));
+  p.part_o = p.part_lse + align256(sizeof(float) * size_t(prefix_slots(b, g, hq)) * q8::kPrefixRows) / sizeof(float);
+  p.flags = status_flags;
+  const int ctas = sms * q8::q8_tc_ctas_per_sm();
+  p.grid = ctas < q8::kPrefixMaxCtas ? ctas : q8::kPrefixMaxCtas;
   q8::TcArgs a = {};
   a.o = o;
-  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q = p.q;
   a.ke = k_exps;
   a.ve = v_exps;
   a.lens = lens;
-  a.pke = prefix_k_exps;
-  a.pve = prefix_v_exps;
-  a.plen = prefix_len;
   a.b = b;
   a.h = h;
   a.g = g;
   a.hq = hq;
   a.m = m_s;
-  a.m_p = m_p;
-  a.spb = q8::q8_shared_block(hq);
-  a.nblk = (b + a.spb - 1) / a.spb;
-  a.nseq = a.nblk + b;
-  a.cols = a.spb * hq;
+  a.partials = 1;
+  a.groups = q8::tc_groups(ctas, g);
   a.scale = scale;
-  a.ws = carve_workspace(workspace, a.nseq, g, a.cols);
+  a.ws = carve_workspace(workspace, b, g, hq);
   a.flags = status_flags;
-  a.grid = sms;
-  const cudaError_t e = q8::launch_q8_decode_shared(a, static_cast<const uint8_t*>(prefix_k),
-                                                    static_cast<const uint8_t*>(prefix_v),
-                                                    static_cast<const uint8_t*>(k_codes),
-                                                    static_cast<const uint8_t*>(v_codes), stream);
-  if (e == cudaErrorInvalidValue) return MQA_ERR_INVALID_ARG;   // sizes past the kernel's index range
+  cudaError_t e = q8::launch_q8_prefix(p, static_cast<const uint8_t*>(prefix_k), static_cast<const uint8_t*>(prefix_v), stream);
+  if (e == cudaSuccess)
+    e = q8::launch_q8_decode_tc(a, static_cast<const uint8_t*>(k_codes), static_cast<const uint8_t*>(v_codes), stream);
+  if (e == cudaSuccess) e = q8::launch_q8_merge(a, &p, stream);
   return e == cudaSuccess ? MQA_OK : MQA_ERR_CUDA;
 }
 

@@ -1,0 +1,163 @@
+// Pieces shared by the tensor-core kernels over 8-bit caches: paired fp32
+// arithmetic, the two-term e4m3 split of queries and weights, tensor maps.
+#pragma once
+
+#include <atomic>
+#include <cuda.h>
+
+#include "q8.cuh"
+#include "sm100.cuh"
+
+namespace mqa {
+namespace q8 {
+
+constexpr int kD = 128;                          // head size
+constexpr uint64_t kTimeoutNs = 1000000000ull;   // of any wait
+constexpr float kLogCodeMax = 8.807354922f;      // log2(448)
+constexpr int kSpan = 60;                        // value exponents below E - kSpan count as E - kSpan in the references
+
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Four floats of shared memory as two pairs.
+__device__ __forceinline__ void load_pairs(const float* p, uint64_t& a, uint64_t& b) {
+  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+  a = v.x;
+  b = v.y;
+}
+
+// Two weights -> their two e4m3 terms (two codes each).  The difference is
+// taken in fp16: its 11 bits hold what the second term's 4 can use.
+__device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+  const __half2 p = __floats2half2_rn(p0, p1);
+  const uint32_t pu = *reinterpret_cast<const uint32_t*>(&p);
+  uint16_t h, l;
+  uint32_t fu;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(pu));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(fu) : "h"(h));
+  const __half2 f = *reinterpret_cast<const __half2*>(&fu);
+  const __half2 d = __hmul2(__hsub2(p, f), __float2half2_rn(16.f));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&d)));
+  hi = h;
+  lo = l;
+}
+
+// The same with the second term unscaled (both then go into one accumulator);
+// returns the weights in fp16, infinite where they pass its range.
+__device__ __forceinline__ __half2 split2_plain(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+  const __half2 p = __floats2half2_rn(p0, p1);
+  uint16_t h, l;
+  uint32_t fu;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(*reinterpret_cast<const uint32_t*>(&p)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(fu) : "h"(h));
+  const __half2 d = __hsub2(p, *reinterpret_cast<const __half2*>(&fu));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&d)));
+  hi = h;
+  lo = l;
+  return p;
+}
+
+// Sixteen elements of a bf16 query row (zeros when row == nullptr) as two e4m3
+// terms of x / s, sixteen codes each; eight neighbouring lanes hold a row
+// (lane part = threadIdx.x % 8) and find its power-of-two scale s, which is
+// returned.  x / s reaches (224, 448]; the second term is the rest itself, so
+// both products add up in one accumulator.  A bf16 element of x / s
+// is exact from 2^-2 on and off by at most 2^-10 below, 2^-17 of the largest.
+__device__ __forceinline__ float split_query(const __nv_bfloat16* row, int part, uint4& hi, uint4& lo) {
+  uint4 w[2] = {};
+  if (row != nullptr) {
+    w[0] = *reinterpret_cast<const uint4*>(row + part * 16);
+    w[1] = *reinterpret_cast<const uint4*>(row + part * 16 + 8);
+  }
+  float x[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t u = k < 4 ? (&w[0].x)[k] : (&w[1].x)[k - 4];
+    const float2 f = bf16x2_to_f32x2(u);
+    x[2 * k] = f.x;
+    x[2 * k + 1] = f.y;
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) amax = fabsf(x[k]) < INFINITY ? fmaxf(amax, fabsf(x[k])) : amax;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const uint32_t e = exponent_for(amax);
+  const float inv = inverse_scale(e);
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t h2[2], l2[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float y[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const float v = x[4 * k + 2 * j + z];
+        y[z] = fabsf(v) < INFINITY ? v * inv : NAN;   // an infinite query gives NaN logits, not saturated ones
+      }
+      h2[j] = to_e4m3x2(y[0], y[1]);
+      const float2 f = from_e4m3x2(h2[j]);
+      l2[j] = to_e4m3x2(y[0] - f.x, y[1] - f.y);
+    }
+    h[k] = h2[0] | (h2[1] << 16);
+    l[k] = l2[0] | (l2[1] << 16);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  return scale_of(e);
+}
+
+// ------------------------------------------------------------------ host
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn encode_fn() {
+  static std::atomic<EncodeTiledFn> cached{nullptr};
+  EncodeTiledFn fn = cached.load(std::memory_order_relaxed);
+  if (fn == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      cached.store(fn = reinterpret_cast<EncodeTiledFn>(p), std::memory_order_relaxed);
+  }
+  return fn;
+}
+
+// Codes [rows, g, 128] as (128, g, rows); a box is `box_rows` rows of one K/V
+// head.  L2 promotion of 128 bytes: a row of one head is all that is used, and
+// 256 would fetch its neighbour's too.
+inline bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int g, int box_rows) {
+  const cuuint64_t dims[3] = {cuuint64_t(kD), cuuint64_t(g), cuuint64_t(rows)};
+  const cuuint64_t strides[2] = {cuuint64_t(kD), cuuint64_t(g) * kD};
+  const cuuint32_t box[3] = {kD, 1, cuuint32_t(box_rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace q8
+}  // namespace mqa

@@ -81,6 +81,29 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
   }
 }
 
+// mbar_wait whose polls may sleep in hardware until the phase completes (up to
+// `kHintNs` each) instead of returning at once: several CTAs' waiting warps
+// then leave the issue slots to the ones that compute.
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  constexpr uint32_t kHintNs = 20000;
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kHintNs)
+        : "memory");
+    if (ok != 0) return true;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    else if (now - t0 > timeout_ns) return false;
+  }
+}
+
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {

@@ -7,10 +7,15 @@ output computed with |V|; L the largest sum of |q_c k_c| * |scale|):
    (numerator and denominator), a sum of n terms by (n + 16) u32 (the 16 covers
    the exponential's and the division's ulps):
        A (2 (d + 4) u32 L + (n + 16) u32);
- - the tensor-core path rounds a weight to two e4m3 terms, at most 2^-9 of it,
-   and the smallest weights to a grid of 2^-20 of the largest p_t s_t (s_t the
-   value row's scale, codes up to 448), half a step each:
-       2^-9 A + n 2^-20 max_t(p_t s_t) 448;
+ - the tensor-core paths round a query's small elements to 2^-10 units of which
+   its largest has at least 224: a logit moves by 2^-10 / 224 max|q| sum|k_c|
+   |scale|, a weight relatively by twice that (M its largest value):
+       A 2 (2^-10 / 224) M;
+   a weight to two e4m3 terms, at most 2^-9 of it, and the smallest weights to
+   a grid: either steps of 2^-13 where the largest p_t s_t (s_t the value row's
+   scale) is at least 2^3, or steps of 2^-9 where it is at least 2^6; half a
+   step each is 2^-16 of the largest at most, times codes up to 448:
+       2^-9 A + n 2^-16 max_t(p_t s_t) 448;
  - bf16 outputs are rounded once: 2^-8 |o| (half a step), fp32: u32 |o|.
 """
 import numpy as np
@@ -76,7 +81,9 @@ def attention(q, parts, g, scale, dtype, two_terms):
             L = (np.abs(qs) @ np.abs(K[:, j]).T).max() * abs(scale)
             t = A * (2 * (d_k + 4) * U32 * L + (n + 16) * U32)
             if two_terms:
-                t = t + 2.0 ** -9 * A + n * 2.0 ** -20 * (w * S[:, j]).max(1, keepdims=True) * 448
+                M = np.abs(qs).max(1, keepdims=True) * np.abs(K[:, j]).sum(1).max() * abs(scale)
+                t = t + A * 2 * 2.0 ** -10 / 224 * M
+                t = t + 2.0 ** -9 * A + n * 2.0 ** -16 * (w * S[:, j]).max(1, keepdims=True) * 448
             t = t + np.abs(ref) * (2.0 ** -8 if dtype == "bf16" else U32)
             o[s, j * hq:(j + 1) * hq], tol[s, j * hq:(j + 1) * hq] = ref, t
     return o, tol
