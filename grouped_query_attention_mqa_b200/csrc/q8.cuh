@@ -112,8 +112,23 @@ cudaError_t launch_q8_decode_tc(const TcArgs& a, const uint8_t* k, const uint8_t
 constexpr int kPrefixRows = 128, kPrefixKeys = 64;   // query rows of a block, keys of a tile
 constexpr int kPrefixMaxCtas = 512;
 __device__ __forceinline__ int prefix_tiles(int len) { return (len + kPrefixKeys - 1) / kPrefixKeys; }
-// CTAs that share `total` tiles.
-__device__ __forceinline__ int prefix_ctas(int64_t total, int grid) { return int(total < grid ? total : int64_t(grid)); }
+// How CTAs share the segments' tiles (`segs` of `nb` each, fewer than 2^31): the
+// first `more` CTAs take `each` + 1 of them, the others `each`.
+struct PrefixShare {
+  int each, more;
+  __device__ __forceinline__ int start(int cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ int owner(int tile) const {
+    const int split = more * (each + 1);
+    return tile < split ? tile / (each + 1) : more + (tile - split) / each;
+  }
+};
+__device__ __forceinline__ PrefixShare prefix_share(int segs, int nb, int grid) {
+  const int total = segs * nb, ctas = min(total, grid);
+  PrefixShare s;
+  s.each = total / ctas;
+  s.more = total - s.each * ctas;
+  return s;
+}
 struct PrefixArgs {
   const __nv_bfloat16* q;
   const uint8_t* ke;     // exponents [g, m_p]

@@ -465,12 +465,18 @@ __device__ __forceinline__ void convert_queries(const TcArgs& a, const Roles& r,
   unsigned char* qs = r.smem + C::kQ;
   float* qw = reinterpret_cast<float*>(r.smem + C::kQw);
   const int part = tid & 7;
+  constexpr int kPasses = HP * 8 / C::kSoft;
+  QueryPiece q[kPasses];   // all loads first
 #pragma unroll
-  for (int pass = 0; pass < HP * 8 / C::kSoft; ++pass) {
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int n = pass * (C::kSoft / 8) + (tid >> 3);
+    q[pass] = load_query(n < a.hq ? a.q + (int64_t(seq) * a.h + int64_t(r.head) * a.hq + n) * kD : nullptr, part);
+  }
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
     const int n = pass * (C::kSoft / 8) + (tid >> 3);
     uint4 hi, lo;
-    const float s = split_query(
-        n < a.hq ? a.q + (int64_t(seq) * a.h + int64_t(r.head) * a.hq + n) * kD : nullptr, part, hi, lo);
+    const float s = split_query(q[pass], hi, lo);
     unsigned char* at = qs + n * 128 + ((part ^ (n & 7)) << 4);   // HP is a multiple of 8: both terms' rows swizzle alike
     *reinterpret_cast<uint4*>(at) = hi;
     *reinterpret_cast<uint4*>(at + C::kQTerm) = lo;
@@ -882,7 +888,10 @@ __global__ void __launch_bounds__(Cfg<HP>::kThreads, kCtasPerSm)
   // The barriers are initialised before the schedule starts loads on them.
   __syncthreads();
   // Inputs may come from the kernel before this one on the stream (the append).
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Beside a prefix kernel nothing is read that it writes, and it has let this
+  // grid start only after its own wait for what came before: that wait stands
+  // for this one's, which comes at the end, for the merge.
+  if (!a.partials) asm volatile("griddepcontrol.wait;" ::: "memory");
   int* lens_tab = reinterpret_cast<int*>(r.smem + C::kLens);
   r.lens_s = lens_tab;
   r.seq0 = 0;
@@ -931,6 +940,7 @@ __global__ void __launch_bounds__(Cfg<HP>::kThreads, kCtasPerSm)
   __syncthreads();
   tc_fence_after();
   if (warp == kSWarp) tmem_dealloc(r.tmem, C::kTmemCols);
+  if (a.partials) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
 }
 

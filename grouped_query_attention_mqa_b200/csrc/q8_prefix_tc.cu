@@ -73,8 +73,7 @@ struct Roles {
   volatile int* abort;
   int32_t* flags;
   int nb;                // tiles per segment
-  int64_t t0;            // the CTA's first tile
-  int n;                 // and its tiles
+  int t0, n;             // the CTA's first tile, and how many it has
   int len;               // prefix rows
 };
 
@@ -87,12 +86,11 @@ __device__ __forceinline__ bool wait_bar(const Roles& r, uint32_t bar, uint32_t 
 
 // Walks the CTA's tiles: segment and tile within it.
 struct Walk {
-  int64_t seg;
-  int k, nb, piece;      // piece: segments met so far, less one
+  int seg, k, nb, piece; // piece: segments met so far, less one
   bool first;
   __device__ Walk(const Roles& r) : nb(r.nb), piece(-1), first(false) {
     seg = r.t0 / nb;
-    k = int(r.t0 - seg * nb) - 1;
+    k = r.t0 - seg * nb - 1;
   }
   __device__ void next() {
     first = piece < 0;
@@ -121,7 +119,7 @@ __device__ void producer(const PrefixArgs& a, const Roles& r, const CUtensorMap*
     const int st = i % S;
     if (i >= S && !wait_bar(r, bar(kEmpty + st), uint32_t(i / S - 1) & 1)) break;
     mbar_expect_tx(bar(kFull + st), kTileBytes);
-    tma_load_3d(r.sbase + kRing + st * kTileBytes, map, bar(kFull + st), 0, int(w.seg / a.blocks), w.k * kKeys, pol);
+    tma_load_3d(r.sbase + kRing + st * kTileBytes, map, bar(kFull + st), 0, w.seg / a.blocks, w.k * kKeys, pol);
   }
   // every copy issued has landed before the CTA can exit
   for (int j = (i - S > 0 ? i - S : 0); j < i; ++j) mbar_wait_asleep(bar(kFull + j % S), uint32_t(j / S) & 1, kTimeoutNs);
@@ -196,7 +194,7 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
   uint32_t nke[2], nve[2];
   auto load_exps = [&]() {
     const int k0 = w.k * kKeys + 2 * lane;
-    const int64_t at = (w.seg / a.blocks) * a.m_p + k0;
+    const int64_t at = int64_t(w.seg / a.blocks) * a.m_p + k0;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       nke[x] = k0 + x < r.len ? a.ke[at + x] : 0u;
@@ -204,17 +202,23 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
     }
   };
   // The block's queries, eight threads per row.
-  auto convert = [&](int64_t seg) {
-    const int head = int(seg / a.blocks);
-    const int64_t r0 = (seg - int64_t(head) * a.blocks) * kRows;
+  auto convert = [&](int seg) {
+    const int head = seg / a.blocks;
+    const int64_t r0 = int64_t(seg - head * a.blocks) * kRows;
     const int part = tid & 7;
-#pragma unroll 2
+    QueryPiece q[8];   // all loads first
+#pragma unroll
+    for (int pass = 0; pass < 8; ++pass) {
+      const int64_t at = r0 + pass * 16 + (tid >> 3);
+      const int s = int(uint32_t(at) / uint32_t(a.hq));   // rows number less than 2^31
+      q[pass] = load_query(
+          at < rows_all ? a.q + (int64_t(s) * a.h + int64_t(head) * a.hq + (at - int64_t(s) * a.hq)) * kD : nullptr, part);
+    }
+#pragma unroll
     for (int pass = 0; pass < 8; ++pass) {
       const int n = pass * 16 + (tid >> 3);
-      const int64_t at = r0 + n, s = at / a.hq;
       uint4 hi, lo;
-      const float sc = split_query(
-          at < rows_all ? a.q + (s * a.h + int64_t(head) * a.hq + (at - s * a.hq)) * kD : nullptr, part, hi, lo);
+      const float sc = split_query(q[pass], hi, lo);
       unsigned char* dst = r.smem + Cfg::kQ + n * 128 + ((part ^ (n & 7)) << 4);
       *reinterpret_cast<uint4*>(dst) = hi;
       *reinterpret_cast<uint4*>(dst + kTermBytes) = lo;
@@ -240,7 +244,7 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
   bool failed = !query_scale(0, rw);
   for (int i = 0; i < r.n && !failed; ++i) {
     const bool first = w.first;
-    const int64_t seg = w.seg;
+    const int seg = w.seg;
     const int valid = min(kKeys, r.len - w.k * kKeys);
     // This tile's scales to the warp's tables
     uint32_t ke[2] = {nke[0], nke[1]}, ve[2] = {nve[0], nve[1]};
@@ -404,16 +408,18 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
       tc_fence_after();
       const int64_t slot = int64_t(blockIdx.x) + seg;
       const float inv = scale_of(uint32_t(E)) * (1.f / (1 << kBias)) * rcp_approx(l);
-      float4* dst = reinterpret_cast<float4*>(a.part_o + (slot * kRows + row) * kD);
-      const bool mine = (seg % a.blocks) * kRows + row < rows_all;
+      float* dst = a.part_o + (slot * kRows + row) * kD;
+      const bool mine = int64_t(seg % a.blocks) * kRows + row < rows_all;
 #pragma unroll
       for (int ch = 0; ch < kD / 32; ++ch) {
         float v[32];
         tmem_ld32(t_lane + kOCol + ch * 32, v);
         if (mine) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[ch * 8 + k] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
+          for (int k = 0; k < 32; k += 8)   // 32 bytes per lane: whole sectors
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + ch * 32 + k), "f"(v[k] * inv),
+                         "f"(v[k + 1] * inv), "f"(v[k + 2] * inv), "f"(v[k + 3] * inv), "f"(v[k + 4] * inv),
+                         "f"(v[k + 5] * inv), "f"(v[k + 6] * inv), "f"(v[k + 7] * inv) : "memory");
         }
       }
       if (mine) a.part_lse[slot * kRows + row] = lg2_approx(l) - negm;
@@ -475,17 +481,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   tc_fence_after();
   r.tmem = *reinterpret_cast<volatile uint32_t*>(r.smem + Cfg::kTmemSlot);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The own rows' kernel may start as this one's CTAs leave room: it reads
+  // nothing of this grid's.
+  asm volatile("griddepcontrol.launch_dependents;");
   const int given = __ldg(a.len);
   r.len = min(max(given, 0), a.m_p);
   if (r.len != given && blockIdx.x == 0 && threadIdx.x == 0) set_flag(a.flags, MQA_FLAG_LEN_CLAMPED);
   r.nb = prefix_tiles(r.len);
-  const int64_t total = int64_t(a.g) * a.blocks * r.nb;
-  const int ctas = prefix_ctas(total, a.grid);
   r.t0 = 0;
   r.n = 0;
-  if (int(blockIdx.x) < ctas) {
-    r.t0 = range_start(blockIdx.x, total, ctas);
-    r.n = int(range_start(int64_t(blockIdx.x) + 1, total, ctas) - r.t0);
+  if (r.nb > 0) {
+    const int total = a.g * a.blocks * r.nb;
+    if (int(blockIdx.x) < total) {
+      const PrefixShare share = prefix_share(a.g * a.blocks, r.nb, a.grid);
+      r.t0 = share.start(blockIdx.x);
+      r.n = share.start(blockIdx.x + 1) - r.t0;
+    }
   }
   if (warp >= kSoftWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
@@ -504,7 +515,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(r.tmem, kTmemCols);
-  asm volatile("griddepcontrol.launch_dependents;");
 }
 
 }  // namespace

@@ -76,18 +76,24 @@ __device__ __forceinline__ __half2 split2_plain(float p0, float p1, uint32_t& hi
   return p;
 }
 
-// Sixteen elements of a bf16 query row (zeros when row == nullptr) as two e4m3
-// terms of x / s, sixteen codes each; eight neighbouring lanes hold a row
-// (lane part = threadIdx.x % 8) and find its power-of-two scale s, which is
-// returned.  x / s reaches (224, 448]; the second term is the rest itself, so
+// Sixteen elements of a bf16 query row (zeros when row == nullptr), then as two
+// e4m3 terms of x / s, sixteen codes each; eight neighbouring lanes hold a row
+// (part = lane % 8) and find its power-of-two scale s, which is returned.  x / s reaches (224, 448]; the second term is the rest itself, so
 // both products add up in one accumulator.  A bf16 element of x / s
 // is exact from 2^-2 on and off by at most 2^-10 below, 2^-17 of the largest.
-__device__ __forceinline__ float split_query(const __nv_bfloat16* row, int part, uint4& hi, uint4& lo) {
-  uint4 w[2] = {};
+struct QueryPiece {
+  uint4 w[2];
+};
+__device__ __forceinline__ QueryPiece load_query(const __nv_bfloat16* row, int part) {
+  QueryPiece q = {};
   if (row != nullptr) {
-    w[0] = *reinterpret_cast<const uint4*>(row + part * 16);
-    w[1] = *reinterpret_cast<const uint4*>(row + part * 16 + 8);
+    q.w[0] = *reinterpret_cast<const uint4*>(row + part * 16);
+    q.w[1] = *reinterpret_cast<const uint4*>(row + part * 16 + 8);
   }
+  return q;
+}
+__device__ __forceinline__ float split_query(const QueryPiece& q, uint4& hi, uint4& lo) {
+  const uint4(&w)[2] = q.w;
   float x[16];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
