@@ -13,6 +13,7 @@ namespace {
 using namespace mqa;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 bool valid_dtype(int dt) { return dt == MQA_F32 || dt == MQA_BF16; }
 bool all_aligned16(std::initializer_list<const void*> ps) {   // and not NULL
@@ -36,7 +37,7 @@ int sm_count() {
   return n;
 }
 
-// Head sizes of the append and the read: a row's 8-element pieces fill 2 to 32
+// Head sizes of the append and the read: a row's 16-element pieces fill 1 to 16
 // lanes, a power of two.
 bool row_width(int d) { return d == 16 || d == 32 || d == 64 || d == 128 || d == 256; }
 
@@ -50,7 +51,7 @@ mqa_status_t check_rows(const void* k, const void* ke, const void* v, const void
     *done = true;
     return MQA_OK;
   }
-  if (!all_aligned16({k, v, kp, vp}) || !ke || !ve) return MQA_ERR_INVALID_ARG;
+  if (!all_aligned16({k, v}) || !kp || !vp || !aligned32(kp) || !aligned32(vp) || !ke || !ve) return MQA_ERR_INVALID_ARG;
   if (int64_t(b) * g > (int64_t(1) << 30) || int64_t(b) * m_max * g > (int64_t(1) << 40) || g > (1 << 20))
     return MQA_ERR_INVALID_ARG;
   if (!row_width(d_k) || !row_width(d_v)) return MQA_ERR_UNSUPPORTED;

@@ -8,11 +8,11 @@
 // e4m3.  Bound: HBM (2 or 4 bytes read and one written per element; the read
 // the other way round); a decode step's few rows are bound by the launch.
 //
-// Both kernels give every thread 8 elements, so d / 8 neighbouring lanes hold
-// a row and find its maximum with shuffles: each byte is read once, in one
-// pass.  A block takes `rows` consecutive packed rows of all heads, which are
-// contiguous in the packed array; its first threads look the rows' sequences
-// up (a binary search in the cumulative counts) once for all heads.
+// Both kernels give every thread 16 elements (32-byte loads and stores of bf16,
+// 16-byte ones of codes), so d / 16 neighbouring lanes hold a row and find its
+// maximum with shuffles: each byte is read once, in one pass.  A block takes `rows` consecutive packed rows of all heads, which are
+// contiguous in the packed array, and looks their sequences up once for all
+// heads.
 #include "q8.cuh"
 
 namespace mqa {
@@ -23,59 +23,131 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxRows = 256;   // packed rows per block
 
-// (sequence, cache row) of every packed row of the block, or (-1, 0).
-__device__ __forceinline__ void locate_rows(int2* where, int r0, int rows, int total, const int32_t* first,
-                                            const int32_t* cu, int b, int m_max, int32_t* flags) {
-  for (int i = threadIdx.x; i < rows; i += kThreads) {
-    const int r = r0 + i;
-    int2 at = make_int2(-1, 0);
-    if (r < total) {
-      int s = r, off = 0;
-      bool mine = true;
-      if (cu != nullptr) {
-        int lo = 0, hi = b;   // the last s with cu[s] <= r
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (__ldg(cu + mid) <= r) lo = mid;
-          else hi = mid;
-        }
-        const int c0 = __ldg(cu + lo);
-        s = lo;
-        off = r - c0;
-        mine = c0 <= r && c0 >= 0 && r < __ldg(cu + lo + 1);   // holds whatever the counts are
-      }
-      if (mine) {
-        const int64_t p = int64_t(first != nullptr ? __ldg(first + s) : 0) + off;
-        if (p >= 0 && p < m_max) at = make_int2(s, int(p));
-        else set_flag(flags, MQA_FLAG_POS_SKIPPED);
-      }
-    }
-    where[i] = at;
+// Where a packed row lives in the cache: its row among all (sequence, row)
+// pairs, and the place of its first head's exponent; `row` < 0: nowhere.
+struct __align__(16) Place {
+  int64_t row, exp;
+};
+
+// The places of packed rows r0 .. r0 + rows - 1 of the block.  Every thread looks
+// at a sequence (one round of independent loads); those with rows in the block
+// have them written down by their warp.  Whatever the counts are, only
+// rows of the block and of the cache are named.
+__device__ __forceinline__ void locate_rows(Place* where, int r0, int rows, const int32_t* first, const int32_t* cu, int b,
+                                            int m_max, int g, int32_t* flags) {
+  auto place = [&](int s, int64_t p) {
+    Place at = {-1, 0};
+    if (p >= 0 && p < m_max) at = {int64_t(s) * m_max + p, int64_t(s) * g * m_max + p};
+    else set_flag(flags, MQA_FLAG_POS_SKIPPED);
+    return at;
+  };
+  if (cu == nullptr) {   // row r is sequence r's
+    for (int i = threadIdx.x; i < rows; i += kThreads)
+      where[i] = place(r0 + i, first != nullptr ? __ldg(first + r0 + i) : 0);
+    __syncthreads();
+    return;
   }
+  for (int i = threadIdx.x; i < rows; i += kThreads) where[i] = {-1, 0};
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  for (int s0 = int(threadIdx.x) - lane; s0 < b; s0 += kThreads) {
+    const int s = s0 + lane;
+    int lo = 0, hi = 0;
+    int64_t p = 0;       // cache row of the first of this sequence's rows in the block
+    if (s < b) {
+      const int c0 = __ldg(cu + s), c1 = __ldg(cu + s + 1);
+      const int64_t p0 = first != nullptr ? __ldg(first + s) : 0;
+      lo = max(c0, r0);
+      hi = c0 < 0 ? lo : min(c1, r0 + rows);
+      p = p0 + (int64_t(lo) - c0);
+    }
+    uint32_t found = __ballot_sync(0xffffffffu, lo < hi);
+    while (found != 0) {   // the warp's lanes share each such sequence's rows
+      const int x = __ffs(found) - 1;
+      found &= found - 1;
+      const int xlo = __shfl_sync(0xffffffffu, lo, x), xhi = __shfl_sync(0xffffffffu, hi, x);
+      const int64_t xp = __shfl_sync(0xffffffffu, (long long)p, x);
+      for (int r = xlo + lane; r < xhi; r += 32) where[r - r0] = place(s0 + x, xp + (r - xlo));
+    }
+  }
+  __syncthreads();
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-  const float2 a = bf16x2_to_f32x2(w.x), b = bf16x2_to_f32x2(w.y), c = bf16x2_to_f32x2(w.z), d = bf16x2_to_f32x2(w.w);
-  x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y, x[4] = c.x, x[5] = c.y, x[6] = d.x, x[7] = d.y;
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  uint32_t w[4];
+
+// Sixteen elements as they lie in memory.
+template <typename T>
+struct Piece;
+
+template <>
+struct Piece<__nv_bfloat16> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { load32(p, w); }
+  // Largest magnitude as a pair of bf16 patterns (NaNs are passed over);
+  // infinities left out if `finite`.
+  __device__ __forceinline__ uint32_t top(bool finite) const {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&t);
+    for (int k = 0; k < 8; ++k) {
+      uint32_t u = w[k] & 0x7fff7fffu;
+      if (finite) {
+        if ((u & 0xffffu) >= 0x7f80u) u &= 0xffff0000u;
+        if ((u >> 16) >= 0x7f80u) u &= 0xffffu;
+      }
+      m = join(m, u);
+    }
+    return m;
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
+  static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  // The joined maximum's fp32 pattern.
+  static __device__ __forceinline__ uint32_t pattern(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
+  __device__ __forceinline__ float2 pair(int k) const { return bf16x2_to_f32x2(w[k]); }
+  __device__ __forceinline__ void set(int k, float x, float y) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
+    w[k] = *reinterpret_cast<const uint32_t*>(&t);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { store32(p, w); }
+};
+
+template <>
+struct Piece<float> {
+  uint32_t w[16];
+  __device__ __forceinline__ void load(const float* p) {
+    load32(p, w);
+    load32(p + 8, w + 8);
+  }
+  __device__ __forceinline__ uint32_t top(bool finite) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      uint32_t u = w[k] & 0x7fffffffu;
+      if (finite && u >= 0x7f800000u) u = 0;
+      m = max(m, u);
+    }
+    return m;
+  }
+  static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t pattern(uint32_t m) { return m; }
+  __device__ __forceinline__ float2 pair(int k) const { return make_float2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1])); }
+  __device__ __forceinline__ void set(int k, float x, float y) {
+    w[2 * k] = __float_as_uint(x);
+    w[2 * k + 1] = __float_as_uint(y);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    store32(p, w);
+    store32(p + 8, w + 8);
+  }
+};
 
 struct CacheArgs {
   uint8_t* codes[2];        // K, V
@@ -83,15 +155,18 @@ struct CacheArgs {
   void* packed[2];          // new rows, or rows read
   const int32_t* first;     // cache row of each sequence's first packed row
   const int32_t* cu;
-  int b, total, m_max, g, lanes_log2[2];   // lanes_log2: log2 of d / 8
+  int b, total, m_max, g, lanes_log2[2];   // lanes_log2: log2 of d / 16
   int rows;                 // packed rows per block
+  unsigned g_inverse;       // floor(2^32 / g) + 1 (g > 1), or 0 where a block has one row
   int32_t* flags;
 };
 
 // blockIdx.y: K or V.  kRead: cache -> packed rows, else packed rows -> cache.
-template <typename T, bool kRead>
+// Bound by instructions as much as by HBM: a thread's elements are kept as
+// they lie in memory, maxima are taken on their bit patterns.
+template <typename T, bool kRead, int kAtOnce>
 __global__ void __launch_bounds__(kThreads) q8_cache_kernel(const CacheArgs a) {
-  __shared__ int2 where[kMaxRows];
+  __shared__ Place where[kMaxRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // What follows on the stream may set up now; it waits for this grid's writes.
   asm volatile("griddepcontrol.launch_dependents;");
@@ -100,53 +175,75 @@ __global__ void __launch_bounds__(kThreads) q8_cache_kernel(const CacheArgs a) {
   const int ll = val ? a.lanes_log2[1] : a.lanes_log2[0], g = a.g;
   uint8_t* const codes = val ? a.codes[1] : a.codes[0];
   uint8_t* const exps = val ? a.exps[1] : a.exps[0];
-  locate_rows(where, r0, a.rows, a.total, a.first, a.cu, a.b, a.m_max, a.flags);
-  __syncthreads();
   const int rows = min(a.rows, a.total - r0);
-  const int n = (rows * g) << ll;                          // 8-element pieces of this block
-  T* const packed = static_cast<T*>(val ? a.packed[1] : a.packed[0]) + ((int64_t(r0) * g) << (ll + 3));
+  locate_rows(where, r0, rows, a.first, a.cu, a.b, a.m_max, g, a.flags);
+  const int n = (rows * g) << ll;                          // pieces of this block
+  T* const packed = static_cast<T*>(val ? a.packed[1] : a.packed[0]) + ((int64_t(r0) * g) << (ll + 4));
   const int lane_mask = (1 << ll) - 1;
-#pragma unroll 4
-  for (int i0 = 0; i0 < n; i0 += kThreads) {               // uniform: the shuffles below are warp-wide
-    const int i = i0 + int(threadIdx.x);
-    const bool in = i < n;
-    const int item = in ? i >> ll : 0, row = item / g, head = item - row * g;
-    const int2 at = in ? where[row] : make_int2(-1, 0);
-    const int c8 = (i & lane_mask) * 8;
-    const int64_t code_at = (((int64_t(at.x) * a.m_max + at.y) * g + head) << (ll + 3)) + c8;
-    const int64_t exp_at = (int64_t(at.x) * g + head) * a.m_max + at.y;
-    if constexpr (kRead) {
-      if (at.x >= 0) {
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + code_at);
-        const float s = scale_of(exps[exp_at]);
-        float x[8];
+  // kAtOnce pieces per thread, their loads all in flight before the first is used
+  for (int i0 = threadIdx.x; i0 - int(threadIdx.x) < n; i0 += kAtOnce * kThreads) {   // uniform: shuffles below
+    int64_t code_at[kAtOnce], exp_at[kAtOnce];
+    Piece<T> x[kAtOnce];
+    uint4 w[kAtOnce];
+    uint32_t e[kAtOnce];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 v = from_e4m3x2((k < 2 ? w.x : w.y) >> (16 * (k & 1)));
-          x[2 * k] = v.x * s;
-          x[2 * k + 1] = v.y * s;
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kThreads;
+      const int item = i >> ll, row = g == 1 ? item : int(__umulhi(unsigned(item), a.g_inverse)),
+                head = item - row * g;
+      const Place at = i < n ? where[row] : Place{-1, 0};
+      code_at[u] = at.row < 0 ? -1 : ((at.row * g + head) << (ll + 4)) + (i & lane_mask) * 16;
+      exp_at[u] = at.exp + int64_t(head) * a.m_max;
+      if constexpr (kRead) {
+        if (code_at[u] >= 0) {
+          w[u] = *reinterpret_cast<const uint4*>(codes + code_at[u]);
+          e[u] = exps[exp_at[u]];
         }
-        store8(packed + int64_t(i) * 8, x);
-      }
-    } else {
-      float x[8] = {};
-      if (at.x >= 0) load8(packed + int64_t(i) * 8, x);
-      float amax = 0.f;
+      } else {
+        if (code_at[u] >= 0) {
+          x[u].load(packed + int64_t(i) * 16);
+        } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float m = fabsf(x[k]);
-        amax = m < INFINITY ? fmaxf(amax, m) : amax;       // finite values only
+          for (int k = 0; k < 8; ++k) x[u].set(k, 0.f, 0.f);
+        }
       }
-      for (int o = 1; o <= lane_mask; o <<= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const uint32_t e = exponent_for(amax);
-      const float inv = inverse_scale(e);
-      if (at.x >= 0) {
-        uint32_t w[4];
+    }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = to_e4m3x2(x[2 * k] * inv, x[2 * k + 1] * inv);
-        *reinterpret_cast<uint2*>(codes + code_at) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-        if ((i & lane_mask) == 0) exps[exp_at] = uint8_t(e);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kThreads;
+      if constexpr (kRead) {
+        if (code_at[u] >= 0) {
+          const float s = scale_of(e[u]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float2 v = from_e4m3x2((&w[u].x)[k / 2] >> (16 * (k & 1)));
+            x[u].set(k, v.x * s, v.y * s);
+          }
+          x[u].store(packed + int64_t(i) * 16);
+        }
+      } else {
+        auto row_top = [&](bool finite) {
+          uint32_t m = x[u].top(finite);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < ll) m = Piece<T>::join(m, __shfl_xor_sync(0xffffffffu, m, 1 << k));
+          return Piece<T>::pattern(m);
+        };
+        uint32_t top = row_top(false);
+        if (__any_sync(0xffffffffu, top >= 0x7f800000u)) top = row_top(true);   // finite values only
+        const uint32_t ex = exponent_for(__uint_as_float(top));
+        const float inv = inverse_scale(ex);
+        if (code_at[u] >= 0) {
+          uint32_t c[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float2 v = x[u].pair(k);
+            c[k] = to_e4m3x2(v.x * inv, v.y * inv);
+          }
+          *reinterpret_cast<uint4*>(codes + code_at[u]) = make_uint4(c[0] | (c[1] << 16), c[2] | (c[3] << 16), c[4] | (c[5] << 16),
+                                                                    c[6] | (c[7] << 16));
+          if ((i & lane_mask) == 0) exps[exp_at[u]] = uint8_t(ex);
+        }
       }
     }
   }
@@ -154,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) q8_cache_kernel(const CacheArgs a) {
 
 int log2_lanes(int d) {
   int l = 0;
-  while ((8 << l) < d) ++l;
+  while ((16 << l) < d) ++l;
   return l;
 }
 
@@ -162,12 +259,15 @@ template <bool kRead>
 cudaError_t launch(CacheArgs& a, int d_k, int d_v, mqa_dtype_t dtype, cudaStream_t stream) {
   a.lanes_log2[0] = log2_lanes(d_k);
   a.lanes_log2[1] = log2_lanes(d_v);
-  // Four passes of the block per tile where that leaves every SM several
-  // blocks, one otherwise (a decode step: as many blocks as there is work for).
-  const int64_t pieces = int64_t(a.g) * ((d_k > d_v ? d_k : d_v) / 8);
-  const int64_t per = int64_t(a.total) * pieces >= int64_t(148) * 8 * kThreads * 4 ? 4 * kThreads : kThreads;
-  const int64_t rows = per / pieces;
+  // Two pieces per thread and step, four steps, where that leaves every SM
+  // several blocks; one piece otherwise (a decode step: as many blocks as there
+  // is work for).
+  const int64_t pieces = int64_t(a.g) * ((d_k > d_v ? d_k : d_v) / 16);
+  const bool large = int64_t(a.total) * pieces >= int64_t(148) * 4 * kThreads * 8;
+  const int64_t rows = (large ? 8 * kThreads : kThreads) / pieces;
   a.rows = int(rows < 1 ? 1 : (rows > kMaxRows ? kMaxRows : rows));
+  // exact for the block's rows x heads, at most 8 kThreads pieces when it has several rows
+  a.g_inverse = a.rows == 1 ? 0u : unsigned((uint64_t(1) << 32) / unsigned(a.g)) + 1u;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((a.total + a.rows - 1) / a.rows), 2);
   cfg.blockDim = dim3(kThreads);
@@ -177,8 +277,11 @@ cudaError_t launch(CacheArgs& a, int d_k, int d_v, mqa_dtype_t dtype, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (dtype == MQA_BF16) return cudaLaunchKernelEx(&cfg, q8_cache_kernel<__nv_bfloat16, kRead>, a);
-  return cudaLaunchKernelEx(&cfg, q8_cache_kernel<float, kRead>, a);
+  if (dtype == MQA_BF16)
+    return large ? cudaLaunchKernelEx(&cfg, q8_cache_kernel<__nv_bfloat16, kRead, 2>, a)
+                 : cudaLaunchKernelEx(&cfg, q8_cache_kernel<__nv_bfloat16, kRead, 1>, a);
+  return large ? cudaLaunchKernelEx(&cfg, q8_cache_kernel<float, kRead, 2>, a)
+               : cudaLaunchKernelEx(&cfg, q8_cache_kernel<float, kRead, 1>, a);
 }
 
 }  // namespace
@@ -187,7 +290,7 @@ cudaError_t launch_q8_append(uint8_t* k, uint8_t* ke, uint8_t* v, uint8_t* ve, c
                              const int32_t* pos, const int32_t* cu, int b, int total, int m_max, int g, int d_k,
                              int d_v, mqa_dtype_t dtype, int32_t* flags, cudaStream_t stream) {
   CacheArgs a = {{k, v}, {ke, ve}, {const_cast<void*>(k_new), const_cast<void*>(v_new)}, pos, cu, b, total, m_max, g,
-                 {0, 0}, 0, flags};
+                 {0, 0}, 0, 0, flags};
   return launch<false>(a, d_k, d_v, dtype, stream);
 }
 
@@ -195,7 +298,7 @@ cudaError_t launch_q8_read(void* k_out, void* v_out, const uint8_t* k, const uin
                            const uint8_t* ve, const int32_t* start, const int32_t* cu, int b, int total, int m_max,
                            int g, int d_k, int d_v, mqa_dtype_t dtype, int32_t* flags, cudaStream_t stream) {
   CacheArgs a = {{const_cast<uint8_t*>(k), const_cast<uint8_t*>(v)}, {const_cast<uint8_t*>(ke), const_cast<uint8_t*>(ve)},
-                 {k_out, v_out}, start, cu, b, total, m_max, g, {0, 0}, 0, flags};
+                 {k_out, v_out}, start, cu, b, total, m_max, g, {0, 0}, 0, 0, flags};
   return launch<true>(a, d_k, d_v, dtype, stream);
 }
 

@@ -11,9 +11,18 @@
 //
 // Work is split as in the other decodes: persistent CTAs over contiguous runs
 // of 64-row tiles, partials of split segments combined by the merge kernel.
-// Bound: FFMA for groups of a few heads (the codes are converted once per four
-// lanes of a row and used for all heads of the group), HBM below that.  Per
-// tile, codes staged by 16-byte cp.async, double buffered:
+//
+// Up to four heads per group and equal widths: q8_decode_rows_kernel.  D / 16
+// lanes hold a row, sixteen codes each, straight from global memory (no shared
+// memory, no barrier until a segment ends); every such group of lanes keeps a
+// softmax of its own over the rows it meets, four rows to a step, and the
+// groups' results are joined at the end.  Bound: HBM latency at these sizes.
+// 12 sequences, 8 K/V heads of 64, windows of up to 1500 rows, fp32, two heads
+// each: 25.5 us with the tile kernel.
+//
+// Otherwise q8_decode_simt_kernel.  Bound: FFMA (the codes are converted once
+// per four lanes of a row and used for all heads of the group).  Per tile, codes
+// staged by 16-byte cp.async, double buffered:
 //   logits   four lanes share a row, each taking every fourth word of codes;
 //            a word becomes four floats in registers, multiplied with every
 //            head's query (16-byte broadcast reads of shared memory);
@@ -291,6 +300,211 @@ __global__ void __launch_bounds__(kThreads, HT == 4 ? 3 : 2) q8_decode_simt_kern
   asm volatile("griddepcontrol.launch_dependents;");
 }
 
+// ------------------------------------------------------------------ groups of few heads
+
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// The codes of a word's k-th half as two fp32.
+__device__ __forceinline__ uint64_t code_pair(const uint4& w, int k) {
+  const float2 f = from_e4m3x2((&w.x)[k / 2] >> (16 * (k & 1)));
+  return pack2(f.x, f.y);
+}
+
+constexpr int kRowThreads = 128, kRowWarps = kRowThreads / 32;
+
+template <int D, int HT>
+__global__ void __launch_bounds__(kRowThreads, HT <= 2 ? 4 : 3) q8_decode_rows_kernel(const DecodeQ8Args a, int is_f32) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;    // lanes per row, rows per warp and load
+  constexpr int kAtOnce = HT <= 2 ? 4 : 2;               // rows of a lane group per step
+  __shared__ int64_t red[kRowWarps + kRowThreads + 2];
+  __shared__ float4 o_s[kRowWarps][HT][D / 4];
+  __shared__ float m_s[kRowWarps][HT], l_s[kRowWarps][HT];
+  const int hq = a.hq, g = a.g;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = lane % kLanes, group = lane / kLanes;
+  const float qscale = a.scale * kLog2e;
+
+  auto store = [&](int64_t at, float x) {
+    if (is_f32) static_cast<float*>(a.o)[at] = x;
+    else static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(x);
+  };
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Sched sc = make_schedule<kRowThreads>(a.lens, a.b, g, a.m_max, a.window, kTile, a.grid, blockIdx.x, a.flags, red);
+  if (a.no_merge) {
+    for (int s = blockIdx.x; s < a.b; s += gridDim.x)
+      if (clamp_len(__ldg(a.lens + s), a.m_max, nullptr, false) == 0)
+        for (int k = threadIdx.x; k < a.h * D; k += kRowThreads) store(int64_t(s) * a.h * D + k, 0.f);
+  }
+  if (sc.t_begin >= sc.t_end) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    return;
+  }
+  Cursor cur = cursor_at(a.lens, a.m_max, a.window, kTile, sc.seq, sc.seq_base);
+  for (int64_t t = sc.t_begin; t < sc.t_end;) {
+    cursor_seek(cur, a.lens, g, a.m_max, a.window, kTile, t);
+    const TileCoord tc = tile_coord(cur, g, kTile, t);
+    // the CTA's tiles of this segment: rows tc.row0 .. row_end - 1
+    const int64_t t_next = min(sc.t_end, tc.seg_t0 + tc.nb);
+    const int row_end = min(cur.len, tc.row0 + int(t_next - t) * kTile);
+    const uint8_t* const k_at = a.k + ((int64_t(tc.seq) * a.m_max) * g + tc.head) * D + part * 16;
+    const uint8_t* const v_at = a.v + ((int64_t(tc.seq) * a.m_max) * g + tc.head) * D + part * 16;
+    const int64_t e0 = (int64_t(tc.seq) * g + tc.head) * a.m_max;
+    uint64_t q[HT][8], o[HT][8];
+    float m[HT], l[HT];
+#pragma unroll
+    for (int i = 0; i < HT; ++i) {
+      const int64_t at = (int64_t(tc.seq) * a.h + int64_t(tc.head) * hq + i) * D + part * 16;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float2 f = make_float2(0.f, 0.f);
+        if (i < hq)
+          f = is_f32 ? static_cast<const float2*>(a.q)[at / 2 + k]
+                     : __bfloat1622float2(static_cast<const __nv_bfloat162*>(a.q)[at / 2 + k]);
+        q[i][k] = pack2(f.x * qscale, f.y * qscale);
+        o[i][k] = 0;
+      }
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+    for (int r0 = tc.row0 + (warp * kAtOnce) * kRows + group; r0 - group < row_end; r0 += kRowWarps * kAtOnce * kRows) {
+      uint4 kc[kAtOnce], vc[kAtOnce];
+      uint32_t ke[kAtOnce], ve[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int r = r0 + u * kRows;
+        kc[u] = vc[u] = make_uint4(0, 0, 0, 0);
+        ke[u] = ve[u] = 0;
+        if (r < row_end) {
+          kc[u] = *reinterpret_cast<const uint4*>(k_at + int64_t(r) * g * D);
+          vc[u] = *reinterpret_cast<const uint4*>(v_at + int64_t(r) * g * D);
+          ke[u] = a.ke[e0 + r];
+          ve[u] = a.ve[e0 + r];
+        }
+      }
+      float s[HT][kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        uint64_t dot[HT];
+#pragma unroll
+        for (int i = 0; i < HT; ++i) dot[i] = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t c = code_pair(kc[u], k);
+#pragma unroll
+          for (int i = 0; i < HT; ++i) dot[i] = fma2(q[i][k], c, dot[i]);
+        }
+        const float ks = scale_of(ke[u]);
+#pragma unroll
+        for (int i = 0; i < HT; ++i) {
+          const float2 f = unpack2(dot[i]);
+          float x = f.x + f.y;
+#pragma unroll
+          for (int w = 1; w < kLanes; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+          s[i][u] = r0 + u * kRows < row_end ? x * ks : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < HT; ++i) {
+        float mn = m[i];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) mn = fmaxf(mn, s[i][u]);
+        const float ref = mn == -INFINITY ? 0.f : mn;   // no row yet
+        const float alpha = exp2f(m[i] - ref);
+        m[i] = mn;
+        l[i] *= alpha;
+        const uint64_t alpha2 = pack2(alpha, alpha);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[i][k] = fma2(o[i][k], alpha2, 0);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const float p = exp2f(s[i][u] - ref);
+          l[i] += p;
+          s[i][u] = p * scale_of(ve[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t c = code_pair(vc[u], k);
+#pragma unroll
+          for (int i = 0; i < HT; ++i) o[i][k] = fma2(pack2(s[i][u], s[i][u]), c, o[i][k]);
+        }
+    }
+    // Join the lane groups, then the warps, in a fixed order.
+#pragma unroll
+    for (int i = 0; i < HT; ++i) {
+      float mw = m[i];
+#pragma unroll
+      for (int w = kLanes; w < 32; w <<= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, w));
+      const float f = exp2f(m[i] - (mw == -INFINITY ? 0.f : mw));
+      float lw = l[i] * f;
+#pragma unroll
+      for (int w = kLanes; w < 32; w <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, w);
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 y = unpack2(o[i][k]);
+        x[2 * k] = y.x * f;
+        x[2 * k + 1] = y.y * f;
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+#pragma unroll
+        for (int w = kLanes; w < 32; w <<= 1) x[k] += __shfl_xor_sync(0xffffffffu, x[k], w);
+      if (group == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o_s[warp][i][part * 4 + k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+      }
+      if (lane == 0) {
+        m_s[warp][i] = mw;
+        l_s[warp][i] = lw;
+      }
+    }
+    __syncthreads();
+    const bool owns_first = tc.seg_t0 >= sc.t_begin;
+    const bool whole = owns_first && tc.seg_t0 + tc.nb <= sc.t_end;
+    const int64_t slot = partial_slot(blockIdx.x, tc.seg);
+    for (int f = threadIdx.x; f < hq * D; f += kRowThreads) {
+      const int i = f / D, c = f - i * D;
+      float mx = m_s[0][i];
+#pragma unroll
+      for (int w = 1; w < kRowWarps; ++w) mx = fmaxf(mx, m_s[w][i]);
+      float sum = 0.f, x = 0.f;   // some row is valid, so mx is finite (or everything is NaN)
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) {
+        const float e = exp2f(m_s[w][i] - mx);
+        sum += l_s[w][i] * e;
+        x += reinterpret_cast<const float*>(o_s[w][i])[c] * e;
+      }
+      x /= sum;
+      if (whole) store((int64_t(tc.seq) * a.h + int64_t(tc.head) * hq + i) * D + c, x);
+      else a.ws.part_o[(slot * hq + i) * D + c] = x;
+      if (!whole && c == 0) a.ws.part_lse[slot * hq + i] = mx + log2f(sum);
+    }
+    if (owns_first && threadIdx.x == 0)
+      a.ws.seg_info[tc.seg] = make_int2(blockIdx.x, cta_of_tile(tc.seg_t0 + tc.nb - 1, sc.total, sc.active));
+    __syncthreads();   // the tables are free for the next segment
+    t = t_next;
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+
+// ------------------------------------------------------------------ host
+
 template <int DK, int DV, int HT>
 cudaError_t ensure_smem_attr() {
   static std::atomic<bool> done[64];   // per device; any thread may set it (the call is idempotent)
@@ -306,24 +520,22 @@ cudaError_t ensure_smem_attr() {
   return e;
 }
 
-template <int DK, int DV, int HT>
-cudaError_t launch(const DecodeQ8Args& a, int is_f32, cudaStream_t stream) {
-  cudaError_t e = ensure_smem_attr<DK, DV, HT>();
-  if (e != cudaSuccess) return e;
+template <typename Kernel>
+cudaError_t launch(Kernel kernel, int threads, size_t smem, const DecodeQ8Args& a, int is_f32, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.grid));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Layout<DK, DV>::bytes(a.hq);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q8_decode_simt_kernel<DK, DV, HT>, a, is_f32);
+  return cudaLaunchKernelEx(&cfg, kernel, a, is_f32);
 }
 
-// Resident CTAs per SM, cached per (device, h/g).
+// Resident CTAs per SM of the tile kernel, cached per (device, h/g).
 template <int DK, int DV, int HT>
 int occupancy(int hq) {
   static std::atomic<int> cache[64][129];
@@ -343,12 +555,29 @@ int occupancy(int hq) {
   return n;
 }
 
-// f(DK, DV, HT) for the built widths; four heads at a time for small groups
+// Up to four heads of equal widths take the rows kernel: fn(D, HT).
+bool rows_kernel(int d_k, int d_v, int hq) { return d_k == d_v && hq <= 4; }
+
+template <typename F>
+auto dispatch_rows(int d, int hq, F&& fn) {
+  auto heads = [&](auto w) {
+    if (hq == 1) return fn(w, std::integral_constant<int, 1>());
+    if (hq == 2) return fn(w, std::integral_constant<int, 2>());
+    return fn(w, std::integral_constant<int, 4>());
+  };
+  if (d == 32) return heads(std::integral_constant<int, 32>());
+  if (d == 64) return heads(std::integral_constant<int, 64>());
+  return heads(std::integral_constant<int, 128>());
+}
+
+// fn(DK, DV, HT) for the built widths; four heads at a time for small groups
 // (fewer registers, more CTAs per SM), sixteen otherwise.
 template <typename F>
-auto dispatch(int d_k, int d_v, int hq, F&& f) {
+auto dispatch(int d_k, int d_v, int hq, F&& fn) {
   auto heads = [&](auto dk, auto dv) {
-    return hq <= 4 ? f(dk, dv, std::integral_constant<int, 4>()) : f(dk, dv, std::integral_constant<int, 16>());
+    if constexpr (decltype(dk)::value != decltype(dv)::value)   // small groups of equal widths have a kernel of their own
+      if (hq <= 4) return fn(dk, dv, std::integral_constant<int, 4>());
+    return fn(dk, dv, std::integral_constant<int, 16>());
   };
   auto values = [&](auto dk) {
     if (d_v == 32) return heads(dk, std::integral_constant<int, 32>());
@@ -363,14 +592,23 @@ auto dispatch(int d_k, int d_v, int hq, F&& f) {
 }  // namespace
 
 cudaError_t launch_q8_decode_simt(const DecodeQ8Args& a, mqa_dtype_t dtype, cudaStream_t stream) {
+  const int is_f32 = dtype == MQA_F32;
+  if (rows_kernel(a.d_k, a.d_v, a.hq))
+    return dispatch_rows(a.d_k, a.hq, [&](auto d, auto ht) {
+      return launch(q8_decode_rows_kernel<decltype(d)::value, decltype(ht)::value>, kRowThreads, 0, a, is_f32, stream);
+    });
   return dispatch(a.d_k, a.d_v, a.hq, [&](auto dk, auto dv, auto ht) {
-    return launch<decltype(dk)::value, decltype(dv)::value, decltype(ht)::value>(a, dtype == MQA_F32, stream);
+    constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value, HT = decltype(ht)::value;
+    const cudaError_t e = ensure_smem_attr<DK, DV, HT>();
+    if (e != cudaSuccess) return e;
+    return launch(q8_decode_simt_kernel<DK, DV, HT>, kThreads, Layout<DK, DV>::bytes(a.hq), a, is_f32, stream);
   });
 }
 
 int q8_simt_tile_rows() { return kTile; }
 
 int q8_simt_ctas_per_sm(int d_k, int d_v, int hq) {
+  if (rows_kernel(d_k, d_v, hq)) return hq <= 2 ? 4 : 3;   // the kernel's launch bounds
   return dispatch(d_k, d_v, hq, [&](auto dk, auto dv, auto ht) {
     return occupancy<decltype(dk)::value, decltype(dv)::value, decltype(ht)::value>(hq);
   });

@@ -23,8 +23,8 @@
  * exponents of one head lie in row order, so a tile's are one short run.
  *
  * Conventions are those of mqa.h: caller-owned device pointers on the current
- * device, 16-byte aligned except the exponent arrays (any alignment), not
- * aliased; dense row-major tensors; asynchronous on `stream`; arguments
+ * device, 16-byte aligned except the exponent arrays (any alignment) and the
+ * packed rows of mqa_q8_append and mqa_q8_read (32-byte aligned), not aliased; dense row-major tensors; asynchronous on `stream`; arguments
  * checked before any launch; no allocation, no state between calls, no
  * exceptions; device-read values are clamped or skipped and reported in
  * *status_flags (NULL to ignore).

@@ -116,6 +116,8 @@ def test_append_and_read_refusals_of_their_own(lib):
     assert _append(lib, cu=None) == INV                   # one row per sequence, yet total != b
     assert _append(lib, pos=None) == INV and _append(lib, kn=ODD) == INV and _append(lib, vn=None) == INV
     assert _read(lib, cu=None) == INV and _read(lib, start=ODD) == INV and _read(lib, ko=None) == INV
+    half = ctypes.c_void_p(0x10010)                       # packed rows: 32-byte aligned
+    assert _append(lib, kn=half) == INV and _read(lib, vo=half) == INV
 
 
 def _decode(lib, **kw):
