@@ -18,7 +18,8 @@
 // softmax of its own over the rows it meets, four rows to a step, and the
 // groups' results are joined at the end.  Bound: HBM latency at these sizes.
 // 12 sequences, 8 K/V heads of 64, windows of up to 1500 rows, fp32, two heads
-// each: 25.5 us with the tile kernel.
+// each: 12.9 us (25.5 with the tile kernel; 15.7 with four CTAs per SM, whose
+// registers spill).
 //
 // Otherwise q8_decode_simt_kernel.  Bound: FFMA (the codes are converted once
 // per four lanes of a row and used for all heads of the group).  Per tile, codes
@@ -326,7 +327,7 @@ __device__ __forceinline__ uint64_t code_pair(const uint4& w, int k) {
 constexpr int kRowThreads = 128, kRowWarps = kRowThreads / 32;
 
 template <int D, int HT>
-__global__ void __launch_bounds__(kRowThreads, HT <= 2 ? 4 : 3) q8_decode_rows_kernel(const DecodeQ8Args a, int is_f32) {
+__global__ void __launch_bounds__(kRowThreads, HT <= 2 ? 3 : 2) q8_decode_rows_kernel(const DecodeQ8Args a, int is_f32) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes;    // lanes per row, rows per warp and load
   constexpr int kAtOnce = HT <= 2 ? 4 : 2;               // rows of a lane group per step
   __shared__ int64_t red[kRowWarps + kRowThreads + 2];
@@ -608,7 +609,7 @@ cudaError_t launch_q8_decode_simt(const DecodeQ8Args& a, mqa_dtype_t dtype, cuda
 int q8_simt_tile_rows() { return kTile; }
 
 int q8_simt_ctas_per_sm(int d_k, int d_v, int hq) {
-  if (rows_kernel(d_k, d_v, hq)) return hq <= 2 ? 4 : 3;   // the kernel's launch bounds
+  if (rows_kernel(d_k, d_v, hq)) return hq <= 2 ? 3 : 2;   // the kernel's launch bounds
   return dispatch(d_k, d_v, hq, [&](auto dk, auto dv, auto ht) {
     return occupancy<decltype(dk)::value, decltype(dv)::value, decltype(ht)::value>(hq);
   });

@@ -3,11 +3,13 @@
 // prefix's blocks.  A part k is a normalised output o_k with lse_k = log2 of
 // its softmax sum; the whole is
 //   o = sum_k 2^(lse_k - m) o_k / sum_k 2^(lse_k - m),   m = max_k lse_k.
-// Bound: latency (a chain of a few L2 round trips), so the work is spread: one
-// CTA of four warps per (sequence, head).  Every warp reads all the parts' lse,
+// Bound: latency (a chain of a few L2 round trips).  An output row has kWarps
+// warps, one for a few parts and four for many.  Each reads all the parts' lse,
 // a lane each (32 at a time), and so knows all weights before it reads outputs;
-// it then sums every fourth part, its lanes four columns each, with the loads
-// of eight parts in flight, and the four sums are added in the warps' order.
+// it then sums its share of the parts, every lane four columns, with the loads
+// of eight parts in flight; the warps' sums are added in their order.  (33 parts
+// behind a 2,000-row prefix: 15 us with one warp a row, 6 with four; 7 parts of
+// 8,192 rows: 8 us with one, 14 with four.)
 #include "q8.cuh"
 
 namespace mqa {
@@ -15,14 +17,19 @@ namespace q8 {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 128, kCtaWarps = kThreads / 32;
 constexpr int kHeadSize = 128;
 constexpr int kAtOnce = 8;
 
-__global__ void __launch_bounds__(32 * kWarps) q8_merge_kernel(const TcArgs a, const PrefixArgs p, int prefix) {
-  __shared__ float4 sums[kWarps - 1][32];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c4 = lane * 4;
-  const int s = int(blockIdx.x / unsigned(a.h)), head = int(blockIdx.x - unsigned(s) * a.h);
+// (sequence, head) of a warp: below 2^31, as the rows of q.
+template <int kWarps>
+__global__ void __launch_bounds__(kThreads) q8_merge_kernel(const TcArgs a, const PrefixArgs p, int prefix) {
+  __shared__ float4 sums[kWarps > 1 ? kWarps - 1 : 1][32];
+  const int warp = kWarps > 1 ? threadIdx.x / 32 : 0, lane = threadIdx.x % 32, c4 = lane * 4;
+  const unsigned items = unsigned(a.b) * unsigned(a.h);
+  const unsigned item = kWarps > 1 ? blockIdx.x : blockIdx.x * kCtaWarps + threadIdx.x / 32;
+  const bool active = item < items;   // warp-uniform; all of a CTA's when its warps share an item
+  const int s = active ? int(item / unsigned(a.h)) : 0, head = active ? int(item - unsigned(s) * a.h) : 0;
   const int j = head / a.hq, i = head - j * a.hq;
   // The lengths are inputs, not written by the kernels this one follows.
   const bool has_own = __ldg(a.lens + s) > 0;
@@ -41,6 +48,7 @@ __global__ void __launch_bounds__(32 * kWarps) q8_merge_kernel(const TcArgs a, c
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
+  if (!active) return;
   int own_first = 0, own_n = 0;
   if (has_own) {
     const int2 info = a.ws.seg_info[int64_t(s) * a.g + j];
@@ -74,53 +82,65 @@ __global__ void __launch_bounds__(32 * kWarps) q8_merge_kernel(const TcArgs a, c
     acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
     m = mn;
     const int cnt = min(32, n - k0);
-    float4 v[kAtOnce];
+    for (int x0 = 0; x0 < cnt; x0 += kWarps * kAtOnce) {   // this warp's parts: warp, warp + kWarps, ...
+      float4 v[kAtOnce];
 #pragma unroll
-    for (int x = 0; x < kAtOnce; ++x) {   // this warp's parts of the 32: warp, warp + 4, ...
-      const float* at = reinterpret_cast<const float*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), warp + kWarps * x));
-      v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (warp + kWarps * x < cnt) v[x] = __ldcg(reinterpret_cast<const float4*>(at + c4));
-    }
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int part = x0 + warp + kWarps * x;
+        const float* at = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), part));
+        v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (part < cnt) v[x] = __ldcg(reinterpret_cast<const float4*>(at + c4));
+      }
 #pragma unroll
-    for (int x = 0; x < kAtOnce; ++x) {   // absent parts have weight 0
-      const float w = __shfl_sync(0xffffffffu, wgt, warp + kWarps * x);
-      acc.x = fmaf(w, v[x].x, acc.x);
-      acc.y = fmaf(w, v[x].y, acc.y);
-      acc.z = fmaf(w, v[x].z, acc.z);
-      acc.w = fmaf(w, v[x].w, acc.w);
+      for (int x = 0; x < kAtOnce; ++x) {   // absent parts have weight 0
+        const float w = __shfl_sync(0xffffffffu, wgt, x0 + warp + kWarps * x);
+        acc.x = fmaf(w, v[x].x, acc.x);
+        acc.y = fmaf(w, v[x].y, acc.y);
+        acc.z = fmaf(w, v[x].z, acc.z);
+        acc.w = fmaf(w, v[x].w, acc.w);
+      }
     }
   }
-  static_assert(kWarps * kAtOnce == 32, "a round covers 32 parts");
-  if (warp > 0) sums[warp - 1][lane] = acc;
-  __syncthreads();
-  if (warp > 0) return;
+  static_assert(32 % (kWarps * kAtOnce) == 0, "whole steps in a round of 32 parts");
+  if constexpr (kWarps > 1) {
+    if (warp > 0) sums[warp - 1][lane] = acc;
+    __syncthreads();
+    if (warp > 0) return;
 #pragma unroll
-  for (int x = 0; x < kWarps - 1; ++x) {
-    const float4 v = sums[x][lane];
-    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    for (int x = 0; x < kWarps - 1; ++x) {
+      const float4 v = sums[x][lane];
+      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
   }
   const float inv = n > 0 ? 1.f / l : 0.f;   // no rows at all: zeros
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   uint2 out;
   out.x = *reinterpret_cast<const uint32_t*>(&lo);
   out.y = *reinterpret_cast<const uint32_t*>(&hi);
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + int64_t(blockIdx.x) * kHeadSize + c4) = out;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + int64_t(item) * kHeadSize + c4) = out;
 }
 
 }  // namespace
 
 cudaError_t launch_q8_merge(const TcArgs& a, const PrefixArgs* prefix, cudaStream_t stream) {
+  // About how many parts a row has: CTAs per segment, and one more at each seam.
+  int parts = a.groups / a.b + 2;
+  if (prefix != nullptr) parts += prefix->grid / (prefix->blocks * a.g) + 2;
+  const bool many = parts > 12;
+  const unsigned items = unsigned(a.b) * unsigned(a.h);   // fewer than 2^31
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(a.b) * unsigned(a.h));   // fewer than 2^31
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.gridDim = dim3(many ? items : (items + kCtaWarps - 1) / kCtaWarps);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q8_merge_kernel, a, prefix != nullptr ? *prefix : PrefixArgs{}, prefix != nullptr ? 1 : 0);
+  const PrefixArgs p = prefix != nullptr ? *prefix : PrefixArgs{};
+  return many ? cudaLaunchKernelEx(&cfg, q8_merge_kernel<kCtaWarps>, a, p, prefix != nullptr ? 1 : 0)
+              : cudaLaunchKernelEx(&cfg, q8_merge_kernel<1>, a, p, prefix != nullptr ? 1 : 0);
 }
 
 }  // namespace q8

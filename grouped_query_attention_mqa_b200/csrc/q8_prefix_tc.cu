@@ -14,17 +14,21 @@
 //   o_r      = 2^(E-6) O[r, :] / l_r
 // Here query rows are the products' M, so that a row's softmax is one thread's
 // own: no barrier and no reduction across threads, and a reference that has to
-// move (some P past 448) concerns its warp alone.  Both terms of P go into one
-// accumulator; the grid that this leaves the small weights is 2^-9 where the
-// largest P is 2^6 or more.
+// move (some P would pass 448) concerns its warp alone.  Both terms of P go into
+// one accumulator; the grid that this leaves the small weights is 2^-9 where
+// the largest P is 2^6 or more.
 //
 // Work: all (head, block) segments have the same number of 64-key tiles; the
 // persistent CTAs take equal contiguous runs of them, and every (CTA, segment)
 // leaves a normalised partial with its log-sum-exp for the merge.  Two CTAs per
 // SM hide each other's chain of product, softmax and product.  Roles: warp 0 K
-// loads, warp 2 V loads, warp 1 S products, warp 3 P.V products (one lane
-// each), warps 4-7 queries, softmax and output, a row per thread.  Every wait is
-// bounded (one second) and reported with MQA_FLAG_PIPE_TIMEOUT.
+// loads, warp 1 S products, warp 3 P.V products (one lane each); warp 2 V loads
+// (one lane) and, with all lanes, the tile's tables: key scales, value factors
+// and exponents, and E, which depend on the cached exponents alone (676 of a
+// tile's 3,700 cycles while the softmax warps made them); warps 4-7 queries,
+// softmax and output, a row per thread.  P has two buffers, so that P(i) need
+// not wait for the product of P(i-1).  Every wait is bounded (one second) and
+// reported with MQA_FLAG_PIPE_TIMEOUT.
 //
 // Bound: the softmax threads' instructions and latency (the products need about
 // 400 cycles per tile and SM, the exponentials 512).
@@ -48,18 +52,21 @@ constexpr uint32_t kTmemCols = 256, kOCol = 2 * kKeys;   // S double buffer, the
 
 struct Cfg {
   static constexpr int kKFull = 0, kKEmpty = kSK, kVFull = 2 * kSK, kVEmpty = kVFull + kSV, kSFull = kVEmpty + kSV,
-                       kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kOFull = kPFull + 1, kQFull = kOFull + 1,
-                       kDone = kQFull + 1, kNumBars = kDone + 1;
+                       kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kOFull = kPFull + 2, kQFull = kOFull + 2,
+                       kTabFull = kQFull + 1, kDone = kTabFull + kSV, kNumBars = kDone + 1;
   static constexpr uint32_t kQ = 0;                                 // two terms
   static constexpr uint32_t kK = kQ + 2 * kTermBytes;
   static constexpr uint32_t kV = kK + kSK * kTileBytes;
   static constexpr uint32_t kP = kV + kSV * kTileBytes;             // a row's line: 64 first terms, 64 second terms
-  static constexpr uint32_t kBar = kP + kRows * 128;
+  static constexpr uint32_t kPBytes = kRows * 128;                  // two such buffers
+  static constexpr uint32_t kBar = kP + 2 * kPBytes;
   static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
   static constexpr uint32_t kAbort = kTmemSlot + 4;
-  static constexpr uint32_t kScales = (kAbort + 4 + 15) / 16 * 16;  // per softmax warp: key scales, value factors, exponents
-  static constexpr uint32_t kWarpScales = 3 * kKeys * 4;
-  static constexpr uint32_t kQw = kScales + 4 * kWarpScales;        // [128] query scales
+  // per V stage: a tile's key scales, value factors, value exponents less E;
+  // then E, and how far it rose with this tile
+  static constexpr uint32_t kTab = (kAbort + 4 + 15) / 16 * 16;
+  static constexpr uint32_t kTabBytes = 3 * kKeys * 4 + 16;
+  static constexpr uint32_t kQw = kTab + kSV * kTabBytes;           // [128] query scales
   static constexpr uint32_t kAlloc = kQw + kRows * 4;
   static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kP % 1024 == 0, "swizzle atoms need 1024-byte alignment");
   static_assert(kAlloc <= (233472 - kCtasPerSm * 1024) / kCtasPerSm, "shared memory budget");
@@ -103,26 +110,101 @@ struct Walk {
   }
 };
 
-template <bool kIsK>
-__device__ void producer(const PrefixArgs& a, const Roles& r, const CUtensorMap* map) {
-  constexpr int S = kIsK ? kSK : kSV;
-  constexpr int kFull = kIsK ? Cfg::kKFull : Cfg::kVFull, kEmpty = kIsK ? Cfg::kKEmpty : Cfg::kVEmpty;
-  constexpr uint32_t kRing = kIsK ? Cfg::kK : Cfg::kV;
-  auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };
-  uint64_t pol;   // the tiles are read again by the other blocks
+__device__ __forceinline__ uint64_t l2_evict_last_policy() {   // the tiles are read again by the other blocks
+  uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+__device__ void k_producer(const PrefixArgs& a, const Roles& r, const CUtensorMap* map) {
+  auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };
+  const uint64_t pol = l2_evict_last_policy();
   Walk w(r);
   int i = 0;
   for (; i < r.n; ++i) {
     w.next();
     if (*r.abort) break;
-    const int st = i % S;
-    if (i >= S && !wait_bar(r, bar(kEmpty + st), uint32_t(i / S - 1) & 1)) break;
-    mbar_expect_tx(bar(kFull + st), kTileBytes);
-    tma_load_3d(r.sbase + kRing + st * kTileBytes, map, bar(kFull + st), 0, w.seg / a.blocks, w.k * kKeys, pol);
+    const int st = i % kSK;
+    if (i >= kSK && !wait_bar(r, bar(Cfg::kKEmpty + st), uint32_t(i / kSK - 1) & 1)) break;
+    mbar_expect_tx(bar(Cfg::kKFull + st), kTileBytes);
+    tma_load_3d(r.sbase + Cfg::kK + st * kTileBytes, map, bar(Cfg::kKFull + st), 0, w.seg / a.blocks, w.k * kKeys, pol);
   }
   // every copy issued has landed before the CTA can exit
-  for (int j = (i - S > 0 ? i - S : 0); j < i; ++j) mbar_wait_asleep(bar(kFull + j % S), uint32_t(j / S) & 1, kTimeoutNs);
+  for (int j = (i - kSK > 0 ? i - kSK : 0); j < i; ++j)
+    mbar_wait_asleep(bar(Cfg::kKFull + j % kSK), uint32_t(j / kSK) & 1, kTimeoutNs);
+}
+
+// V tiles (lane 0) and the tables beside them.  A stage is free again when the
+// P.V product of its tile has completed: every softmax thread has then read the
+// stage's table, too.
+__device__ void v_producer(const PrefixArgs& a, const Roles& r, const CUtensorMap* map, int lane) {
+  auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };
+  const uint64_t pol = l2_evict_last_policy();
+  const float c = a.scale * kLog2e;
+  Walk w(r);
+  // Exponents of keys 2 lane and 2 lane + 1 of the walker's tile.
+  uint32_t ke[2], ve[2];
+  int head = 0;
+  auto load_exps = [&]() {
+    if (w.first) head = w.seg / a.blocks;
+    const int k0 = w.k * kKeys + 2 * lane;
+    const int64_t at = int64_t(head) * a.m_p + k0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      ke[x] = k0 + x < r.len ? a.ke[at + x] : 0u;
+      ve[x] = k0 + x < r.len ? a.ve[at + x] : 0u;
+    }
+  };
+  w.next();
+  load_exps();
+  int E = 0, i = 0;
+  bool any = false;      // some value row of the segment so far was not all zeros
+  for (; i < r.n; ++i) {
+    const int st = i % kSV, k = w.k, at_head = head;
+    const bool first = w.first;
+    bool go = *r.abort == 0;
+    if (i >= kSV) go = mbar_wait_asleep(bar(Cfg::kVEmpty + st), uint32_t(i / kSV - 1) & 1, kTimeoutNs) && go;
+    if (!__all_sync(0xffffffffu, go)) {
+      if (lane == 0) {
+        *r.abort = 1;
+        set_flag(r.flags, MQA_FLAG_PIPE_TIMEOUT);
+      }
+      break;
+    }
+    if (lane == 0) {
+      mbar_expect_tx(bar(Cfg::kVFull + st), kTileBytes);
+      tma_load_3d(r.sbase + Cfg::kV + st * kTileBytes, map, bar(Cfg::kVFull + st), 0, at_head, k * kKeys, pol);
+    }
+    const uint32_t k0 = ke[0], k1 = ke[1], v0 = ve[0], v1 = ve[1];
+    if (i + 1 < r.n) {
+      w.next();
+      load_exps();
+    }
+    const int em = __reduce_max_sync(0xffffffffu, int(max(v0 > 1 ? v0 : 0u, v1 > 1 ? v1 : 0u)));
+    float rise = 0.f;
+    if (first) {
+      E = em > 0 ? em : 119;   // no value yet: a middling 2^-8
+      any = em > 0;
+    } else if (em > E || (em > 0 && !any)) {
+      rise = float(em - E);
+      E = em;
+      any = true;
+    }
+    float* const tab = reinterpret_cast<float*>(r.smem + Cfg::kTab + st * Cfg::kTabBytes);
+    reinterpret_cast<float2*>(tab)[lane] = make_float2(scale_of(k0) * c, scale_of(k1) * c);
+    const int f0 = int(v0) - E + 127 + kBias, f1 = int(v1) - E + 127 + kBias;   // b_t 2^(kBias - E)
+    reinterpret_cast<float2*>(tab + kKeys)[lane] = make_float2(v0 == 0 || f0 <= 0 ? 0.f : __uint_as_float(uint32_t(f0) << 23),
+                                                              v1 == 0 || f1 <= 0 ? 0.f : __uint_as_float(uint32_t(f1) << 23));
+    reinterpret_cast<float2*>(tab + 2 * kKeys)[lane] =
+        make_float2(float(max(int(v0) - E, -kSpan)), float(max(int(v1) - E, -kSpan)));
+    if (lane == 0) reinterpret_cast<float2*>(tab + 3 * kKeys)[0] = make_float2(scale_of(uint32_t(E)), rise);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(Cfg::kTabFull + st));
+  }
+  // every copy issued has landed before the CTA can exit
+  if (lane == 0)
+    for (int j = (i - kSV > 0 ? i - kSV : 0); j < i; ++j)
+      mbar_wait_asleep(bar(Cfg::kVFull + j % kSV), uint32_t(j / kSV) & 1, kTimeoutNs);
 }
 
 __device__ void s_issuer(const Roles& r) {
@@ -159,8 +241,8 @@ __device__ void pv_issuer(const Roles& r) {
   Walk w(r);
   for (int i = 0; i < r.n; ++i) {
     w.next();
-    const int st = i % kSV;
-    if (!wait_bar(r, bar(Cfg::kPFull), uint32_t(i) & 1)) break;
+    const int st = i % kSV, pb = i & 1;
+    if (!wait_bar(r, bar(Cfg::kPFull + pb), uint32_t(i >> 1) & 1)) break;
     if (!wait_bar(r, bar(Cfg::kVFull + st), uint32_t(i / kSV) & 1)) break;
     tc_fence_after();
     const uint64_t va = vdesc0 + uint64_t((uint32_t(st) * kTileBytes) >> 4);
@@ -168,9 +250,9 @@ __device__ void pv_issuer(const Roles& r) {
     for (int term = 0; term < 2; ++term)
 #pragma unroll
       for (int kk = 0; kk < kKeys / 32; ++kk)
-        mma_e4m3_ss(r.tmem + kOCol, pdesc + ((term * kKeys + kk * 32) >> 4), va + ((kk * 4096) >> 4), idesc,
+        mma_e4m3_ss(r.tmem + kOCol, pdesc + ((pb * Cfg::kPBytes + term * kKeys + kk * 32) >> 4), va + ((kk * 4096) >> 4), idesc,
                     !w.first || term + kk > 0);
-    mma_commit(bar(Cfg::kOFull));
+    mma_commit(bar(Cfg::kOFull + pb));
     mma_commit(bar(Cfg::kVEmpty + st));
   }
   mma_commit(bar(Cfg::kDone));
@@ -182,25 +264,11 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
   auto wait = [&](int id, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_asleep(bar(id), parity, kTimeoutNs)); };
   const int q4 = warp & 3, tid = threadIdx.x - 32 * kSoftWarp, row = 32 * q4 + lane;
   const uint32_t t_lane = r.tmem + (uint32_t(32 * q4) << 16);
-  float* const ksc = reinterpret_cast<float*>(r.smem + Cfg::kScales + q4 * Cfg::kWarpScales);
-  float *const vfac = ksc + kKeys, *const vexp = vfac + kKeys;
   float* const qw = reinterpret_cast<float*>(r.smem + Cfg::kQw);
-  unsigned char* const line = r.smem + Cfg::kP + row * 128;
-  const float c = a.scale * kLog2e;
+  unsigned char* const lines = r.smem + Cfg::kP + row * 128;
   const int64_t rows_all = int64_t(a.b) * a.hq;
   Walk w(r);
 
-  // Row exponents of the walker's tile: keys 2 lane and 2 lane + 1.
-  uint32_t nke[2], nve[2];
-  auto load_exps = [&]() {
-    const int k0 = w.k * kKeys + 2 * lane;
-    const int64_t at = int64_t(w.seg / a.blocks) * a.m_p + k0;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      nke[x] = k0 + x < r.len ? a.ke[at + x] : 0u;
-      nve[x] = k0 + x < r.len ? a.ve[at + x] : 0u;
-    }
-  };
   // The block's queries, eight threads per row.
   auto convert = [&](int seg) {
     const int head = seg / a.blocks;
@@ -231,66 +299,42 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
   // next block's come after this one's products, which wait for every thread.)
   auto query_scale = [&](int piece, float& rw) {
     if (!wait(Cfg::kQFull, uint32_t(piece) & 1)) return false;
-    rw = qw[row] * c;
+    rw = qw[row];
     return true;
   };
 
   w.next();
-  load_exps();
   convert(w.seg);
-  float negm = 0.f, l = 0.f, rw = 0.f;
-  int E = 0;             // the value exponent P is relative to
-  bool any = false;      // some value row so far was not all zeros
+  float negm = 0.f, l = 0.f, rw = 0.f;   // minus the row's reference, its sum, its query scale
   bool failed = !query_scale(0, rw);
   for (int i = 0; i < r.n && !failed; ++i) {
     const bool first = w.first;
-    const int seg = w.seg;
+    const int seg = w.seg, st = i % kSV, pb = i & 1;
     const int valid = min(kKeys, r.len - w.k * kKeys);
-    // This tile's scales to the warp's tables
-    uint32_t ke[2] = {nke[0], nke[1]}, ve[2] = {nve[0], nve[1]};
-    if (i + 1 < r.n) {
-      w.next();
-      load_exps();
-    }
+    if (i + 1 < r.n) w.next();
     const bool last = i + 1 == r.n || w.first;
-    const int em = __reduce_max_sync(0xffffffffu, int(max(ve[0] > 1 ? ve[0] : 0u, ve[1] > 1 ? ve[1] : 0u)));
-    if (first) {
-      E = em > 0 ? em : 119;   // no value yet: a middling 2^-8
-      any = em > 0;
-      negm = 0.f;
-      l = 0.f;
-    } else if (em > E || (em > 0 && !any)) {   // the weights are now relative to another exponent, the references with them
-      negm += float(em - E);
-      l *= ex2_approx(float(em - E));
-      E = em;
-      any = true;
-    }
-    {
-      float2 f, x;
-      f.x = scale_of(ke[0]);
-      f.y = scale_of(ke[1]);
-      reinterpret_cast<float2*>(ksc)[lane] = f;
-      const int f0 = int(ve[0]) - E + 127 + kBias, f1 = int(ve[1]) - E + 127 + kBias;   // b_t 2^(kBias - E)
-      f.x = ve[0] == 0 || f0 <= 0 ? 0.f : __uint_as_float(uint32_t(f0) << 23);
-      f.y = ve[1] == 0 || f1 <= 0 ? 0.f : __uint_as_float(uint32_t(f1) << 23);
-      reinterpret_cast<float2*>(vfac)[lane] = f;
-      x.x = float(max(int(ve[0]) - E, -kSpan));
-      x.y = float(max(int(ve[1]) - E, -kSpan));
-      reinterpret_cast<float2*>(vexp)[lane] = x;
-      __syncwarp();
-    }
-    if (!wait(Cfg::kSFull + (i & 1), uint32_t(i >> 1) & 1)) {
+    if (!wait(Cfg::kTabFull + st, uint32_t(i / kSV) & 1) || !wait(Cfg::kSFull + pb, uint32_t(i >> 1) & 1)) {
       failed = true;
       break;
     }
     tc_fence_after();
+    const float* const ksc = reinterpret_cast<const float*>(r.smem + Cfg::kTab + st * Cfg::kTabBytes);
+    const float *const vfac = ksc + kKeys, *const vexp = vfac + kKeys;
+    const float2 tile = reinterpret_cast<const float2*>(vexp + kKeys)[0];   // 2^(E-127), rise of E
+    if (first) {
+      negm = 0.f;
+      l = 0.f;
+    } else if (tile.y != 0.f) {   // the weights are now relative to a larger exponent, the references with them
+      negm += tile.y;
+      l *= ex2_approx(tile.y);
+    }
     uint64_t x[kKeys / 2];     // s - m, in pairs
     {
       const uint64_t rw2 = pack2(rw, rw), m2 = pack2(negm, negm);
 #pragma unroll
       for (int ch = 0; ch < kKeys / 32; ++ch) {
         float s[32];
-        tmem_ld32(t_lane + uint32_t(i & 1) * kKeys + ch * 32, s);
+        tmem_ld32(t_lane + uint32_t(pb) * kKeys + ch * 32, s);
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
           uint64_t k0, k1;
@@ -300,7 +344,7 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
         }
       }
       tc_fence_before();
-      mbar_arrive(bar(Cfg::kSEmpty + (i & 1)));   // the buffer may take S(i+2)
+      mbar_arrive(bar(Cfg::kSEmpty + pb));   // the buffer may take S(i+2)
       if (valid < kKeys) {
 #pragma unroll
         for (int k = 0; k < kKeys / 2; ++k) {
@@ -310,67 +354,64 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
         }
       }
     }
-    // P in two terms; again with moved references if some row's passed 448
-    uint32_t hi[kKeys / 4], lo[kKeys / 4];
+    // The largest P (relative to 2^kBias): does the reference have to move?
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kKeys; k += 4) {
+      uint64_t e0, e1;
+      float y0, y1, y2, y3;
+      load_pairs(vexp + k, e0, e1);
+      unpack2(add2(x[k / 2], e0), y0, y1);
+      unpack2(add2(x[k / 2 + 1], e1), y2, y3);
+      top = fmaxf(fmaxf(top, y0), y1);
+      top = fmaxf(fmaxf(top, y2), y3);
+    }
     float alpha = 1.f;
-    bool move = first, moved = false;
-    uint64_t sum2;
-    for (;;) {
-      if (move) {
-        float top = -INFINITY;
+    bool moved = false;
+    if (__any_sync(0xffffffffu, first || top > kLogCodeMax - kBias)) {
+      const float by = first ? top : fmaxf(top, 0.f);
+      const uint64_t b2 = pack2(-by, -by);
 #pragma unroll
-        for (int k = 0; k < kKeys; k += 4) {
-          uint64_t e0, e1;
-          float y0, y1, y2, y3;
-          load_pairs(vexp + k, e0, e1);
-          unpack2(add2(x[k / 2], e0), y0, y1);
-          unpack2(add2(x[k / 2 + 1], e1), y2, y3);
-          top = fmaxf(fmaxf(top, fmaxf(y0, y1)), fmaxf(y2, y3));
-        }
-        const float by = first ? top : fmaxf(top, 0.f);
-        const uint64_t b2 = pack2(-by, -by);
-#pragma unroll
-        for (int k = 0; k < kKeys / 2; ++k) x[k] = add2(x[k], b2);
-        negm -= by;
-        if (!first) {
-          alpha = ex2_approx(-by);
-          l *= alpha;
-          moved = __any_sync(0xffffffffu, by > 0.f);
-        }
+      for (int k = 0; k < kKeys / 2; ++k) x[k] = add2(x[k], b2);
+      negm -= by;
+      if (!first) {
+        alpha = ex2_approx(-by);
+        l *= alpha;
+        moved = true;
       }
-      sum2 = 0;
-      __half2 big = __float2half2_rn(0.f);
+    }
+    // P in two terms
+    uint32_t hi[kKeys / 4], lo[kKeys / 4];
+    uint64_t sum2 = 0;
 #pragma unroll
-      for (int k4 = 0; k4 < kKeys / 4; ++k4) {
-        uint64_t f[2];
-        load_pairs(vfac + 4 * k4, f[0], f[1]);
-        uint32_t h[2], lw[2];
+    for (int k4 = 0; k4 < kKeys / 4; ++k4) {
+      uint64_t f[2];
+      load_pairs(vfac + 4 * k4, f[0], f[1]);
+      uint32_t h[2], lw[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x0, x1, p0, p1;
-          unpack2(x[2 * k4 + j], x0, x1);
-          const uint64_t e = pack2(ex2_approx(x0), ex2_approx(x1));
-          sum2 = add2(sum2, e);
-          unpack2(mul2(e, f[j]), p0, p1);
-          big = __hmax2(big, split2_plain(p0, p1, h[j], lw[j]));
-        }
-        hi[k4] = h[0] | (h[1] << 16);
-        lo[k4] = lw[0] | (lw[1] << 16);
+      for (int j = 0; j < 2; ++j) {
+        float x0, x1, p0, p1;
+        unpack2(x[2 * k4 + j], x0, x1);
+        const uint64_t e = pack2(ex2_approx(x0), ex2_approx(x1));
+        sum2 = add2(sum2, e);
+        unpack2(mul2(e, f[j]), p0, p1);
+        split2_plain(p0, p1, h[j], lw[j]);
       }
-      const bool over = __half2float(__low2half(big)) > kCodeMax || __half2float(__high2half(big)) > kCodeMax;
-      if (move || !__any_sync(0xffffffffu, over)) break;
-      move = true;
+      hi[k4] = h[0] | (h[1] << 16);
+      lo[k4] = lw[0] | (lw[1] << 16);
     }
     {
       float s0, s1;
       unpack2(sum2, s0, s1);
       l += s0 + s1;
     }
-    // P.V(i-1) must be complete before O is rescaled and P overwritten; a
-    // ragged tile needs its V rows landed before those past the end are zeroed.
+    // P.V(i-2) must be complete before its P is overwritten, P.V(i-1) before O
+    // is rescaled; a ragged tile needs its V rows landed before those past the
+    // end are zeroed.
     bool fine = true;
-    if (i > 0) fine = wait(Cfg::kOFull, uint32_t(i - 1) & 1);
-    if (valid < kKeys) fine = wait(Cfg::kVFull + i % kSV, uint32_t(i / kSV) & 1) && fine;
+    if (i > 1) fine = wait(Cfg::kOFull + pb, uint32_t((i >> 1) - 1) & 1);
+    if (i > 0 && moved) fine = wait(Cfg::kOFull + (pb ^ 1), uint32_t((i - 1) >> 1) & 1) && fine;
+    if (valid < kKeys) fine = wait(Cfg::kVFull + st, uint32_t(i / kSV) & 1) && fine;
     if (!fine) {
       failed = true;
       break;
@@ -387,6 +428,7 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
       }
       tmem_wait_st();
     }
+    unsigned char* const line = lines + pb * Cfg::kPBytes;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       *reinterpret_cast<uint4*>(line + ((j ^ (row & 7)) << 4)) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
@@ -394,20 +436,20 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
           make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
     }
     if (valid < kKeys) {
-      unsigned char* vst = r.smem + Cfg::kV + (i % kSV) * kTileBytes + valid * 128;
+      unsigned char* vst = r.smem + Cfg::kV + st * kTileBytes + valid * 128;
       for (int k = tid; k < (kKeys - valid) * 8; k += kSoft) *reinterpret_cast<uint4*>(vst + k * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    mbar_arrive(bar(Cfg::kPFull));
+    mbar_arrive(bar(Cfg::kPFull + pb));
     if (last) {   // the segment's partial; then the next one's queries (its S products wait for them)
-      if (!wait(Cfg::kOFull, uint32_t(i) & 1)) {
+      if (!wait(Cfg::kOFull + pb, uint32_t(i >> 1) & 1)) {
         failed = true;
         break;
       }
       tc_fence_after();
       const int64_t slot = int64_t(blockIdx.x) + seg;
-      const float inv = scale_of(uint32_t(E)) * (1.f / (1 << kBias)) * rcp_approx(l);
+      const float inv = tile.x * (1.f / (1 << kBias)) * rcp_approx(l);
       float* dst = a.part_o + (slot * kRows + row) * kD;
       const bool mine = int64_t(seg % a.blocks) * kRows + row < rows_all;
 #pragma unroll
@@ -458,13 +500,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int s = 0; s < kSV; ++s) {
       mbar_init(bar(Cfg::kVFull + s), 1);
       mbar_init(bar(Cfg::kVEmpty + s), 1);
+      mbar_init(bar(Cfg::kTabFull + s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(Cfg::kSFull + s), 1);
       mbar_init(bar(Cfg::kSEmpty + s), kSoft);
+      mbar_init(bar(Cfg::kPFull + s), kSoft);
+      mbar_init(bar(Cfg::kOFull + s), 1);
     }
-    mbar_init(bar(Cfg::kPFull), kSoft);
-    mbar_init(bar(Cfg::kOFull), 1);
     mbar_init(bar(Cfg::kQFull), kSoft);
     mbar_init(bar(Cfg::kDone), 2);   // one commit from each issuing thread
     *r.abort = 0;
@@ -503,11 +546,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (r.n > 0) softmax(a, r, warp, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRoles));
-    if (r.n > 0 && lane == 0) {
-      if (warp == 0) producer<true>(a, r, &tm_k);
-      else if (warp == 1) s_issuer(r);
-      else if (warp == 2) producer<false>(a, r, &tm_v);
-      else pv_issuer(r);
+    if (r.n > 0) {
+      if (warp == 2) {
+        v_producer(a, r, &tm_v, lane);
+      } else if (lane == 0) {
+        if (warp == 0) k_producer(a, r, &tm_k);
+        else if (warp == 1) s_issuer(r);
+        else pv_issuer(r);
+      }
     }
     __syncwarp();
   }

@@ -61,9 +61,8 @@ __device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_
   lo = l;
 }
 
-// The same with the second term unscaled (both then go into one accumulator);
-// returns the weights in fp16, infinite where they pass its range.
-__device__ __forceinline__ __half2 split2_plain(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+// The same with the second term unscaled (both then go into one accumulator).
+__device__ __forceinline__ void split2_plain(float p0, float p1, uint32_t& hi, uint32_t& lo) {
   const __half2 p = __floats2half2_rn(p0, p1);
   uint16_t h, l;
   uint32_t fu;
@@ -73,7 +72,6 @@ __device__ __forceinline__ __half2 split2_plain(float p0, float p1, uint32_t& hi
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&d)));
   hi = h;
   lo = l;
-  return p;
 }
 
 // Sixteen elements of a bf16 query row (zeros when row == nullptr), then as two
