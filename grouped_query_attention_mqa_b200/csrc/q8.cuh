@@ -131,18 +131,24 @@ __device__ __forceinline__ PrefixShare prefix_share(int segs, int nb, int grid) 
 }
 struct PrefixArgs {
   const __nv_bfloat16* q;
+  const uint8_t* k;      // codes [m_p, g, d]
   const uint8_t* ke;     // exponents [g, m_p]
+  const uint8_t* v;
   const uint8_t* ve;
   const int32_t* len;    // [1]
   int b, h, g, hq, m_p;
   int blocks;            // blocks of query rows per K/V head
+  int tiles;             // tiles of m_p rows
+  __half* k16;           // unpacked [g, tiles * kPrefixKeys, d]
+  __half* v16;
+  int2* tile_exps;       // [g, tiles]: what the unpacked keys and values are relative to
   float scale;
   float* part_o;         // [slots][kPrefixRows][d], slot = CTA + head * blocks + block
   float* part_lse;       // [slots][kPrefixRows]
   int32_t* flags;
   int grid;
 };
-cudaError_t launch_q8_prefix(const PrefixArgs& a, const uint8_t* k, const uint8_t* v, cudaStream_t stream);
+cudaError_t launch_q8_prefix(const PrefixArgs& a, cudaStream_t stream);
 
 // Joins the partials of the own rows (and of a prefix, if given).
 cudaError_t launch_q8_merge(const TcArgs& a, const PrefixArgs* prefix, cudaStream_t stream);

@@ -204,21 +204,31 @@ mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, const ui
 namespace {
 
 // Workspace of a decode behind a shared prefix: the own rows' partials as for
-// a decode, then the prefix's.
-int64_t prefix_blocks(int b, int hq) { return (int64_t(b) * hq + q8::kPrefixRows - 1) / q8::kPrefixRows; }
-int64_t prefix_slots(int b, int g, int hq) { return q8::kPrefixMaxCtas + prefix_blocks(b, hq) * g; }
-size_t shared_bytes(int b, int g, int hq, int d) {
-  return workspace_bytes(b, g, hq, d) + align256(sizeof(float) * size_t(prefix_slots(b, g, hq)) * q8::kPrefixRows) +
-         sizeof(float) * size_t(prefix_slots(b, g, hq)) * q8::kPrefixRows * size_t(d);
-}
+// a decode, then the prefix's (outputs, log-sum-exps), then the prefix unpacked
+// (keys, values, what its tiles are relative to).
+struct SharedSizes {
+  int64_t blocks, tiles;
+  size_t own, lse, o, rows, exps;   // bytes of each part
+  SharedSizes(int b, int g, int hq, int m_p, int d) {
+    blocks = (int64_t(b) * hq + q8::kPrefixRows - 1) / q8::kPrefixRows;
+    tiles = (int64_t(m_p) + q8::kPrefixKeys - 1) / q8::kPrefixKeys;
+    const size_t part_rows = size_t(q8::kPrefixMaxCtas + blocks * g) * q8::kPrefixRows;
+    own = workspace_bytes(b, g, hq, d);
+    lse = align256(sizeof(float) * part_rows);
+    o = align256(sizeof(float) * part_rows * size_t(d));
+    rows = align256(2 * size_t(g) * size_t(tiles) * q8::kPrefixKeys * size_t(d));
+    exps = align256(sizeof(int2) * size_t(g) * size_t(tiles));
+  }
+  size_t total() const { return own + lse + o + 2 * rows + exps; }
+};
 
 }  // namespace
 
 extern "C" {
 
-size_t mqa_q8_decode_shared_workspace_size(int b, int h, int g, int d) {
-  if (b < 0 || h < 1 || g < 1 || h % g != 0 || d < 1 || h / g > 64) return 0;
-  return shared_bytes(b, g, h / g, d);
+size_t mqa_q8_decode_shared_workspace_size(int b, int h, int g, int m_p, int d) {
+  if (b < 0 || h < 1 || g < 1 || h % g != 0 || m_p < 1 || d < 1 || h / g > 64) return 0;
+  return SharedSizes(b, g, h / g, m_p, d).total();
 }
 
 mqa_status_t mqa_q8_decode_shared(void* o, const void* q, const void* prefix_k, const uint8_t* prefix_k_exps,
@@ -236,18 +246,22 @@ mqa_status_t mqa_q8_decode_shared(void* o, const void* q, const void* prefix_k, 
     return MQA_ERR_INVALID_ARG;
   if (int64_t(b) * g > (int64_t(1) << 29) || int64_t(b) * m_s * g > (int64_t(1) << 40) ||
       int64_t(m_p) * g > (int64_t(1) << 40) || int64_t(b) * h >= (int64_t(1) << 31) || !q8::q8_tc_fits(b, m_s) ||
-      !q8::q8_tc_fits(1, m_p) ||
+      !q8::q8_tc_fits(1, m_p) || g > 65535 ||   // a grid dimension
       ((int64_t(b) * (h / g) + q8::kPrefixRows - 1) / q8::kPrefixRows) * g * ((int64_t(m_p) + q8::kPrefixKeys - 1) / q8::kPrefixKeys) >=
           (int64_t(1) << 31))
     return MQA_ERR_INVALID_ARG;   // past the kernels' index range
   const int hq = h / g;
   if (dtype != MQA_BF16 || !q8::q8_tc_supported(d, d, hq, g)) return MQA_ERR_UNSUPPORTED;
-  if (workspace_bytes_given < mqa_q8_decode_shared_workspace_size(b, h, g, d)) return MQA_ERR_INVALID_ARG;
+  if (workspace_bytes_given < mqa_q8_decode_shared_workspace_size(b, h, g, m_p, d)) return MQA_ERR_INVALID_ARG;
   const int sms = sm_count();
   if (sms <= 0) return MQA_ERR_CUDA;
+  const SharedSizes size(b, g, hq, m_p, d);
+  char* at = static_cast<char*>(workspace) + size.own;
   q8::PrefixArgs p = {};
   p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const uint8_t*>(prefix_k);
   p.ke = prefix_k_exps;
+  p.v = static_cast<const uint8_t*>(prefix_v);
   p.ve = prefix_v_exps;
   p.len = prefix_len;
   p.b = b;
@@ -255,10 +269,14 @@ mqa_status_t mqa_q8_decode_shared(void* o, const void* q, const void* prefix_k, 
   p.g = g;
   p.hq = hq;
   p.m_p = m_p;
-  p.blocks = int(prefix_blocks(b, hq));
+  p.blocks = int(size.blocks);
+  p.tiles = int(size.tiles);
   p.scale = scale;
-  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + workspace_bytes(b, g, hq, d));
-  p.part_o = p.part_lse + align256(sizeof(float) * size_t(prefix_slots(b, g, hq)) * q8::kPrefixRows) / sizeof(float);
+  p.part_lse = reinterpret_cast<float*>(at);
+  p.part_o = reinterpret_cast<float*>(at += size.lse);
+  p.k16 = reinterpret_cast<__half*>(at += size.o);
+  p.v16 = reinterpret_cast<__half*>(at += size.rows);
+  p.tile_exps = reinterpret_cast<int2*>(at += size.rows);
   p.flags = status_flags;
   const int ctas = sms * q8::q8_tc_ctas_per_sm();
   p.grid = ctas < q8::kPrefixMaxCtas ? ctas : q8::kPrefixMaxCtas;
@@ -278,7 +296,7 @@ mqa_status_t mqa_q8_decode_shared(void* o, const void* q, const void* prefix_k, 
   a.scale = scale;
   a.ws = carve_workspace(workspace, b, g, hq);
   a.flags = status_flags;
-  cudaError_t e = q8::launch_q8_prefix(p, static_cast<const uint8_t*>(prefix_k), static_cast<const uint8_t*>(prefix_v), stream);
+  cudaError_t e = q8::launch_q8_prefix(p, stream);
   if (e == cudaSuccess)
     e = q8::launch_q8_decode_tc(a, static_cast<const uint8_t*>(k_codes), static_cast<const uint8_t*>(v_codes), stream);
   if (e == cudaSuccess) e = q8::launch_q8_merge(a, &p, stream);

@@ -3,35 +3,40 @@
 // in blocks of 128 rows, so that a staged tile serves 128 rows and the work is
 // that of a matrix product, not of a stream.
 //
-// The rows of one K/V head j are the pairs (sequence, head of the group), in
-// that order; a block takes 128 of them.  With x = q / w in two e4m3 terms, the
-// codes k, v and the row scales a, b (see the decode kernel for the terms'
-// precision):
-//   S[r, t]  = (x1_r + x2_r) . k_t     M = 128 query rows, N = 64 keys, K = 2 x 128
-//   s_{r,t}  = scale log2(e) w_r a_t S[r, t],   p = 2^(s - m_r),  l_r = sum_t p
-//   P[r, t]  = p b_t 2^(6-E)           in two e4m3 terms P1 + P2, P2 = e4m3(P - P1)
-//   O[r, c] += sum_t (P1 + P2)[r, t] v_t[c]      M = 128, N = 128, K = 2 x 64
-//   o_r      = 2^(E-6) O[r, :] / l_r
+// Two kernels.  The first unpacks the prefix to fp16, once for the whole batch:
+// tile by tile of 64 rows, each tile relative to its largest key and its largest
+// value exponent,
+//   k'_t = code_t 2^(a_t - A),   v'_t = code_t 2^(b_t - B)      (exact: a code has 4 bits; rows
+// 2^-15 and more below their tile's largest lose bits below 2^-24 of a unit of
+// which that has 224), zeros past the prefix's end.  The second is a
+// flash-style product over query blocks: the rows of one K/V head are the pairs
+// (sequence, head of the group), in that order, and with x_r = q_r / w_r in
+// fp16 (maximum in (224, 448], bf16's 8 bits exact to 2^-17 of a unit)
+//   S[r, t]  = x_r . k'_t              M = 128 query rows, N = 64 keys, K = 128
+//   y_{r,t}  = scale log2(e) w_r 2^A S[r, t] + B - B_0
+//   P[r, t]  = 2^(y - M_r)  in fp16    (11 bits: a weight is off by 2^-12 of itself at most)
+//   O[r, c] += sum_t P[r, t] v'_t[c]   M = 128, N = 128, K = 64 keys
+//   l_r     += sum_t P[r, t] 2^(B_0 - B)   in fp32, before P is rounded
+//   o_r      = 2^B_0 O[r, :] / l_r
+// B_0 is the first tile's B: the value exponent enters with the logit, so that a
+// reference M_r is the largest contribution to the output, not the largest
+// weight.  fp16 spans 40 octaves: P starts at 1, a reference moves only when
+// some P would pass 2^15, and what is below 2^-24 of the reference is dropped.
+// (The same product on the e4m3 codes as they are, with both operands in two
+// e4m3 terms and per-row scale tables, took 1.9 times as long: the softmax
+// threads' instructions bound it, and a reference moved every third tile.)
 // Here query rows are the products' M, so that a row's softmax is one thread's
-// own: no barrier and no reduction across threads, and a reference that has to
-// move (some P would pass 448) concerns its warp alone.  Both terms of P go into
-// one accumulator; the grid that this leaves the small weights is 2^-9 where
-// the largest P is 2^6 or more.
+// own: no barrier and no reduction across threads.
 //
-// Work: all (head, block) segments have the same number of 64-key tiles; the
+// Work: all (head, block) segments have the same number of tiles; the
 // persistent CTAs take equal contiguous runs of them, and every (CTA, segment)
 // leaves a normalised partial with its log-sum-exp for the merge.  Two CTAs per
 // SM hide each other's chain of product, softmax and product.  Roles: warp 0 K
-// loads, warp 1 S products, warp 3 P.V products (one lane each); warp 2 V loads
-// (one lane) and, with all lanes, the tile's tables: key scales, value factors
-// and exponents, and E, which depend on the cached exponents alone (676 of a
-// tile's 3,700 cycles while the softmax warps made them); warps 4-7 queries,
-// softmax and output, a row per thread.  P has two buffers, so that P(i) need
-// not wait for the product of P(i-1).  Every wait is bounded (one second) and
-// reported with MQA_FLAG_PIPE_TIMEOUT.
+// loads, warp 2 V loads, warp 1 S products, warp 3 P.V products (one lane
+// each), warps 4-7 queries, softmax and output, a row per thread.  Every wait is
+// bounded (one second) and reported with MQA_FLAG_PIPE_TIMEOUT.
 //
-// Bound: the softmax threads' instructions and latency (the products need about
-// 400 cycles per tile and SM, the exponentials 512).
+// Bound: the softmax threads' instructions and latency.
 #include "q8_tc.cuh"
 
 namespace mqa {
@@ -45,33 +50,101 @@ constexpr int kRows = kPrefixRows, kKeys = kPrefixKeys;
 constexpr int kThreads = 256, kSoft = 128, kSoftWarp = 4;
 constexpr int kCtasPerSm = 2;
 constexpr int kRegsRoles = 72, kRegsSoft = 184;   // of the 128 per thread at launch
-constexpr int kBias = 6;                          // the largest P after a reference is set is 2^kBias
-constexpr int kSK = 2, kSV = 3;                   // ring stages
-constexpr uint32_t kTermBytes = kRows * kD, kTileBytes = kKeys * kD;
+constexpr float kTopP = 32768.f;                  // P stays below it: half of fp16's range
+constexpr int kSK = 2, kSV = 2;                   // ring stages
+constexpr uint32_t kQHalf = kRows * 128, kHalf = kKeys * 128;   // 64 columns: 128-byte swizzled rows
+constexpr uint32_t kTileBytes = 2 * kHalf;
 constexpr uint32_t kTmemCols = 256, kOCol = 2 * kKeys;   // S double buffer, then O
+
+// Instruction descriptor of tcgen05.mma kind::f16 with fp16 inputs (code 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
+  return (1u << 4) | (uint32_t(a_mn_major) << 15) | (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
 
 struct Cfg {
   static constexpr int kKFull = 0, kKEmpty = kSK, kVFull = 2 * kSK, kVEmpty = kVFull + kSV, kSFull = kVEmpty + kSV,
-                       kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kOFull = kPFull + 2, kQFull = kOFull + 2,
-                       kTabFull = kQFull + 1, kDone = kTabFull + kSV, kNumBars = kDone + 1;
-  static constexpr uint32_t kQ = 0;                                 // two terms
-  static constexpr uint32_t kK = kQ + 2 * kTermBytes;
+                       kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kOFull = kPFull + 1, kQFull = kOFull + 1,
+                       kDone = kQFull + 1, kNumBars = kDone + 1;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + 2 * kQHalf;
   static constexpr uint32_t kV = kK + kSK * kTileBytes;
-  static constexpr uint32_t kP = kV + kSV * kTileBytes;             // a row's line: 64 first terms, 64 second terms
-  static constexpr uint32_t kPBytes = kRows * 128;                  // two such buffers
-  static constexpr uint32_t kBar = kP + 2 * kPBytes;
+  static constexpr uint32_t kP = kV + kSV * kTileBytes;             // a row's line: 64 fp16 weights
+  static constexpr uint32_t kBar = kP + kRows * 128;
   static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
   static constexpr uint32_t kAbort = kTmemSlot + 4;
-  // per V stage: a tile's key scales, value factors, value exponents less E;
-  // then E, and how far it rose with this tile
-  static constexpr uint32_t kTab = (kAbort + 4 + 15) / 16 * 16;
-  static constexpr uint32_t kTabBytes = 3 * kKeys * 4 + 16;
-  static constexpr uint32_t kQw = kTab + kSV * kTabBytes;           // [128] query scales
+  static constexpr uint32_t kQw = kAbort + 4;                       // [128] query scales
   static constexpr uint32_t kAlloc = kQw + kRows * 4;
   static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kP % 1024 == 0, "swizzle atoms need 1024-byte alignment");
   static_assert(kAlloc <= (233472 - kCtasPerSm * 1024) / kCtasPerSm, "shared memory budget");
   static_assert(128 * kRegsRoles + kSoft * kRegsSoft == kThreads * 128, "registers");
 };
+
+// ------------------------------------------------------------------ unpacking
+
+constexpr int kUnpackThreads = 256;
+
+// One tile of 64 rows of one K/V head, keys and values, to fp16; (A, B) of the
+// tile beside it.  Bound: HBM (128 + 1 bytes read and 256 written per row).
+__global__ void __launch_bounds__(kUnpackThreads) q8_unpack_kernel(const PrefixArgs a) {
+  __shared__ int top[2][2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tile = blockIdx.x, head = blockIdx.y, warp = threadIdx.x / 32;
+  const int given = __ldg(a.len), len = min(max(given, 0), a.m_p);
+  if (given != len && tile == 0 && head == 0 && threadIdx.x == 0) set_flag(a.flags, MQA_FLAG_LEN_CLAMPED);
+  const int row0 = tile * kKeys;
+  if (row0 >= len) return;
+  // threads 0-63 the keys' exponents, 64-127 the values'
+  const int64_t e_at = int64_t(head) * a.m_p + row0;
+  if (threadIdx.x < 2 * kKeys) {
+    const int t = threadIdx.x % kKeys;
+    const uint8_t* const exps = threadIdx.x < kKeys ? a.ke : a.ve;
+    const uint32_t e = row0 + t < len ? exps[e_at + t] : 0u;
+    const int m = __reduce_max_sync(0xffffffffu, int(e > 1 ? e : 0u));   // rows of zeros aside
+    if (threadIdx.x % 32 == 0) top[warp / 2][warp % 2] = m;
+  }
+  // this thread's pieces: 16 codes each, keys first
+  constexpr int kPieces = 2 * kKeys * (kD / 16) / kUnpackThreads;
+  uint4 w[kPieces];
+  uint32_t e[kPieces];
+#pragma unroll
+  for (int x = 0; x < kPieces; ++x) {
+    const int p = x * kUnpackThreads + threadIdx.x, val = p / (kKeys * (kD / 16));
+    const int t = (p / (kD / 16)) % kKeys, c = p % (kD / 16);
+    w[x] = make_uint4(0, 0, 0, 0);
+    e[x] = 0;
+    if (row0 + t < len) {
+      w[x] = *reinterpret_cast<const uint4*>((val ? a.v : a.k) + ((int64_t(row0) + t) * a.g + head) * kD + c * 16);
+      e[x] = (val ? a.ve : a.ke)[e_at + t];
+    }
+  }
+  __syncthreads();
+  const int top_k = max(top[0][0], top[0][1]), top_v = max(top[1][0], top[1][1]);
+  const int A = max(top_k, 1), B = max(top_v, 1);
+  const int64_t out = (int64_t(head) * a.tiles + tile) * kKeys * kD;
+#pragma unroll
+  for (int x = 0; x < kPieces; ++x) {
+    const int p = x * kUnpackThreads + threadIdx.x, val = p / (kKeys * (kD / 16));
+    const int t = (p / (kD / 16)) % kKeys, c = p % (kD / 16);
+    const int d = int(e[x]) - (val ? B : A);   // 0 at most
+    // rows of the smallest scale count as zeros where a tile's values have no other
+    const bool none = e[x] == 0 || d < -60 || (val && top_v == 0);
+    const __half2 f = __float2half2_rn(none ? 0.f : __uint_as_float(uint32_t(127 + d) << 23));
+    uint32_t h[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t u;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(u) : "h"(uint16_t((&w[x].x)[k / 2] >> (16 * (k & 1)))));
+      const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&u), f);
+      h[k] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    __half* const dst = (val ? a.v16 : a.k16) + out + t * kD + c * 16;
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]),
+                 "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
+  }
+  // a tile whose values are all zeros has no B: 0 tells so
+  if (threadIdx.x == 0) a.tile_exps[head * a.tiles + tile] = make_int2(A, top_v);
+}
 
 struct Roles {
   uint32_t sbase;
@@ -110,105 +183,32 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ uint64_t l2_evict_last_policy() {   // the tiles are read again by the other blocks
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
-}
-
-__device__ void k_producer(const PrefixArgs& a, const Roles& r, const CUtensorMap* map) {
+template <bool kIsK>
+__device__ void producer(const PrefixArgs& a, const Roles& r, const CUtensorMap* map) {
+  constexpr int S = kIsK ? kSK : kSV;
+  constexpr int kFull = kIsK ? Cfg::kKFull : Cfg::kVFull, kEmpty = kIsK ? Cfg::kKEmpty : Cfg::kVEmpty;
+  constexpr uint32_t kRing = kIsK ? Cfg::kK : Cfg::kV;
   auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };
-  const uint64_t pol = l2_evict_last_policy();
+  uint64_t pol;   // the tiles are read again by the other blocks
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
   Walk w(r);
   int i = 0;
   for (; i < r.n; ++i) {
     w.next();
     if (*r.abort) break;
-    const int st = i % kSK;
-    if (i >= kSK && !wait_bar(r, bar(Cfg::kKEmpty + st), uint32_t(i / kSK - 1) & 1)) break;
-    mbar_expect_tx(bar(Cfg::kKFull + st), kTileBytes);
-    tma_load_3d(r.sbase + Cfg::kK + st * kTileBytes, map, bar(Cfg::kKFull + st), 0, w.seg / a.blocks, w.k * kKeys, pol);
+    const int st = i % S;
+    if (i >= S && !wait_bar(r, bar(kEmpty + st), uint32_t(i / S - 1) & 1)) break;
+    const uint32_t dst = r.sbase + kRing + st * kTileBytes;
+    mbar_expect_tx(bar(kFull + st), kTileBytes);
+    tma_load_3d(dst, map, bar(kFull + st), 0, w.k * kKeys, w.seg / a.blocks, pol);
+    tma_load_3d(dst + kHalf, map, bar(kFull + st), 64, w.k * kKeys, w.seg / a.blocks, pol);
   }
   // every copy issued has landed before the CTA can exit
-  for (int j = (i - kSK > 0 ? i - kSK : 0); j < i; ++j)
-    mbar_wait_asleep(bar(Cfg::kKFull + j % kSK), uint32_t(j / kSK) & 1, kTimeoutNs);
-}
-
-// V tiles (lane 0) and the tables beside them.  A stage is free again when the
-// P.V product of its tile has completed: every softmax thread has then read the
-// stage's table, too.
-__device__ void v_producer(const PrefixArgs& a, const Roles& r, const CUtensorMap* map, int lane) {
-  auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };
-  const uint64_t pol = l2_evict_last_policy();
-  const float c = a.scale * kLog2e;
-  Walk w(r);
-  // Exponents of keys 2 lane and 2 lane + 1 of the walker's tile.
-  uint32_t ke[2], ve[2];
-  int head = 0;
-  auto load_exps = [&]() {
-    if (w.first) head = w.seg / a.blocks;
-    const int k0 = w.k * kKeys + 2 * lane;
-    const int64_t at = int64_t(head) * a.m_p + k0;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      ke[x] = k0 + x < r.len ? a.ke[at + x] : 0u;
-      ve[x] = k0 + x < r.len ? a.ve[at + x] : 0u;
-    }
-  };
-  w.next();
-  load_exps();
-  int E = 0, i = 0;
-  bool any = false;      // some value row of the segment so far was not all zeros
-  for (; i < r.n; ++i) {
-    const int st = i % kSV, k = w.k, at_head = head;
-    const bool first = w.first;
-    bool go = *r.abort == 0;
-    if (i >= kSV) go = mbar_wait_asleep(bar(Cfg::kVEmpty + st), uint32_t(i / kSV - 1) & 1, kTimeoutNs) && go;
-    if (!__all_sync(0xffffffffu, go)) {
-      if (lane == 0) {
-        *r.abort = 1;
-        set_flag(r.flags, MQA_FLAG_PIPE_TIMEOUT);
-      }
-      break;
-    }
-    if (lane == 0) {
-      mbar_expect_tx(bar(Cfg::kVFull + st), kTileBytes);
-      tma_load_3d(r.sbase + Cfg::kV + st * kTileBytes, map, bar(Cfg::kVFull + st), 0, at_head, k * kKeys, pol);
-    }
-    const uint32_t k0 = ke[0], k1 = ke[1], v0 = ve[0], v1 = ve[1];
-    if (i + 1 < r.n) {
-      w.next();
-      load_exps();
-    }
-    const int em = __reduce_max_sync(0xffffffffu, int(max(v0 > 1 ? v0 : 0u, v1 > 1 ? v1 : 0u)));
-    float rise = 0.f;
-    if (first) {
-      E = em > 0 ? em : 119;   // no value yet: a middling 2^-8
-      any = em > 0;
-    } else if (em > E || (em > 0 && !any)) {
-      rise = float(em - E);
-      E = em;
-      any = true;
-    }
-    float* const tab = reinterpret_cast<float*>(r.smem + Cfg::kTab + st * Cfg::kTabBytes);
-    reinterpret_cast<float2*>(tab)[lane] = make_float2(scale_of(k0) * c, scale_of(k1) * c);
-    const int f0 = int(v0) - E + 127 + kBias, f1 = int(v1) - E + 127 + kBias;   // b_t 2^(kBias - E)
-    reinterpret_cast<float2*>(tab + kKeys)[lane] = make_float2(v0 == 0 || f0 <= 0 ? 0.f : __uint_as_float(uint32_t(f0) << 23),
-                                                              v1 == 0 || f1 <= 0 ? 0.f : __uint_as_float(uint32_t(f1) << 23));
-    reinterpret_cast<float2*>(tab + 2 * kKeys)[lane] =
-        make_float2(float(max(int(v0) - E, -kSpan)), float(max(int(v1) - E, -kSpan)));
-    if (lane == 0) reinterpret_cast<float2*>(tab + 3 * kKeys)[0] = make_float2(scale_of(uint32_t(E)), rise);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(Cfg::kTabFull + st));
-  }
-  // every copy issued has landed before the CTA can exit
-  if (lane == 0)
-    for (int j = (i - kSV > 0 ? i - kSV : 0); j < i; ++j)
-      mbar_wait_asleep(bar(Cfg::kVFull + j % kSV), uint32_t(j / kSV) & 1, kTimeoutNs);
+  for (int j = (i - S > 0 ? i - S : 0); j < i; ++j) mbar_wait_asleep(bar(kFull + j % S), uint32_t(j / S) & 1, kTimeoutNs);
 }
 
 __device__ void s_issuer(const Roles& r) {
-  constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kKeys, 0, 0);
+  constexpr uint32_t idesc = idesc_f16_f32(kRows, kKeys, 0, 0);
   const uint64_t qdesc = smem_desc_sw128(r.sbase + Cfg::kQ, 16, 1024), kdesc0 = smem_desc_sw128(r.sbase + Cfg::kK, 16, 1024);
   auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };
   Walk w(r);
@@ -221,11 +221,9 @@ __device__ void s_issuer(const Roles& r) {
     tc_fence_after();
     const uint64_t ka = kdesc0 + uint64_t((uint32_t(st) * kTileBytes) >> 4);
 #pragma unroll
-    for (int term = 0; term < 2; ++term)
-#pragma unroll
-      for (int kk = 0; kk < kD / 32; ++kk)
-        mma_e4m3_ss(r.tmem + uint32_t(sb) * kKeys, qdesc + ((term * kTermBytes + kk * 32) >> 4), ka + ((kk * 32) >> 4), idesc,
-                    term + kk > 0);
+    for (int kk = 0; kk < kD / 16; ++kk)
+      mma_bf16_ss(r.tmem + uint32_t(sb) * kKeys, qdesc + (((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4),
+                  ka + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), idesc, kk > 0);
     mma_commit(bar(Cfg::kSFull + sb));
     mma_commit(bar(Cfg::kKEmpty + st));
   }
@@ -234,25 +232,22 @@ __device__ void s_issuer(const Roles& r) {
 }
 
 __device__ void pv_issuer(const Roles& r) {
-  constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kD, 0, 1);
-  const uint64_t pdesc = smem_desc_sw128(r.sbase + Cfg::kP, 16, 1024);    // K-major, both terms in a row's 128 bytes
-  const uint64_t vdesc0 = smem_desc_sw128(r.sbase + Cfg::kV, 16, 1024);   // MN-major: keys are K
+  constexpr uint32_t idesc = idesc_f16_f32(kRows, kD, 0, 1);
+  const uint64_t pdesc = smem_desc_sw128(r.sbase + Cfg::kP, 16, 1024);       // K-major: keys are K
+  const uint64_t vdesc0 = smem_desc_sw128(r.sbase + Cfg::kV, kHalf, 1024);   // MN-major: columns are N
   auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };
   Walk w(r);
   for (int i = 0; i < r.n; ++i) {
     w.next();
-    const int st = i % kSV, pb = i & 1;
-    if (!wait_bar(r, bar(Cfg::kPFull + pb), uint32_t(i >> 1) & 1)) break;
+    const int st = i % kSV;
+    if (!wait_bar(r, bar(Cfg::kPFull), uint32_t(i) & 1)) break;
     if (!wait_bar(r, bar(Cfg::kVFull + st), uint32_t(i / kSV) & 1)) break;
     tc_fence_after();
     const uint64_t va = vdesc0 + uint64_t((uint32_t(st) * kTileBytes) >> 4);
 #pragma unroll
-    for (int term = 0; term < 2; ++term)
-#pragma unroll
-      for (int kk = 0; kk < kKeys / 32; ++kk)
-        mma_e4m3_ss(r.tmem + kOCol, pdesc + ((pb * Cfg::kPBytes + term * kKeys + kk * 32) >> 4), va + ((kk * 4096) >> 4), idesc,
-                    !w.first || term + kk > 0);
-    mma_commit(bar(Cfg::kOFull + pb));
+    for (int kk = 0; kk < kKeys / 16; ++kk)
+      mma_bf16_ss(r.tmem + kOCol, pdesc + ((kk * 32) >> 4), va + ((kk * 2048) >> 4), idesc, !w.first || kk > 0);
+    mma_commit(bar(Cfg::kOFull));
     mma_commit(bar(Cfg::kVEmpty + st));
   }
   mma_commit(bar(Cfg::kDone));
@@ -265,7 +260,8 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
   const int q4 = warp & 3, tid = threadIdx.x - 32 * kSoftWarp, row = 32 * q4 + lane;
   const uint32_t t_lane = r.tmem + (uint32_t(32 * q4) << 16);
   float* const qw = reinterpret_cast<float*>(r.smem + Cfg::kQw);
-  unsigned char* const lines = r.smem + Cfg::kP + row * 128;
+  unsigned char* const line = r.smem + Cfg::kP + row * 128;
+  const float c = a.scale * kLog2e;
   const int64_t rows_all = int64_t(a.b) * a.hq;
   Walk w(r);
 
@@ -285,11 +281,13 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
 #pragma unroll
     for (int pass = 0; pass < 8; ++pass) {
       const int n = pass * 16 + (tid >> 3);
-      uint4 hi, lo;
-      const float sc = split_query(q[pass], hi, lo);
-      unsigned char* dst = r.smem + Cfg::kQ + n * 128 + ((part ^ (n & 7)) << 4);
-      *reinterpret_cast<uint4*>(dst) = hi;
-      *reinterpret_cast<uint4*>(dst + kTermBytes) = lo;
+      uint32_t h[8];
+      const float sc = half_query(q[pass], h);
+      // columns 16 part .. + 15: two 16-byte pieces of the row's line in their 64-column half
+      unsigned char* dst = r.smem + Cfg::kQ + (part >> 2) * kQHalf + n * 128;
+      const int p0 = (part & 3) * 2;
+      *reinterpret_cast<uint4*>(dst + ((p0 ^ (n & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(dst + (((p0 + 1) ^ (n & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
       if (part == 0) qw[n] = sc;
     }
     fence_proxy_async_smem();
@@ -299,120 +297,107 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
   // next block's come after this one's products, which wait for every thread.)
   auto query_scale = [&](int piece, float& rw) {
     if (!wait(Cfg::kQFull, uint32_t(piece) & 1)) return false;
-    rw = qw[row];
+    rw = qw[row] * c;
     return true;
   };
 
   w.next();
+  int2 exps = a.tile_exps[w.seg / a.blocks * a.tiles + w.k];   // the next tile's A and B
   convert(w.seg);
   float negm = 0.f, l = 0.f, rw = 0.f;   // minus the row's reference, its sum, its query scale
+  int B0 = 119;
   bool failed = !query_scale(0, rw);
   for (int i = 0; i < r.n && !failed; ++i) {
     const bool first = w.first;
-    const int seg = w.seg, st = i % kSV, pb = i & 1;
+    const int seg = w.seg;
     const int valid = min(kKeys, r.len - w.k * kKeys);
-    if (i + 1 < r.n) w.next();
+    const int2 e = exps;
+    if (i + 1 < r.n) {
+      w.next();
+      exps = a.tile_exps[w.seg / a.blocks * a.tiles + w.k];
+    }
     const bool last = i + 1 == r.n || w.first;
-    if (!wait(Cfg::kTabFull + st, uint32_t(i / kSV) & 1) || !wait(Cfg::kSFull + pb, uint32_t(i >> 1) & 1)) {
+    if (first) {
+      B0 = e.y > 0 ? e.y : 119;   // no value yet: any exponent does
+      negm = 0.f;
+      l = 0.f;
+    }
+    const int rise = e.y > 0 ? min(max(e.y - B0, -126), 126) : 0;   // B - B_0
+    const float a_t = rw * scale_of(uint32_t(e.x)), shift = float(rise);
+    if (!wait(Cfg::kSFull + (i & 1), uint32_t(i >> 1) & 1)) {
       failed = true;
       break;
     }
     tc_fence_after();
-    const float* const ksc = reinterpret_cast<const float*>(r.smem + Cfg::kTab + st * Cfg::kTabBytes);
-    const float *const vfac = ksc + kKeys, *const vexp = vfac + kKeys;
-    const float2 tile = reinterpret_cast<const float2*>(vexp + kKeys)[0];   // 2^(E-127), rise of E
-    if (first) {
-      negm = 0.f;
-      l = 0.f;
-    } else if (tile.y != 0.f) {   // the weights are now relative to a larger exponent, the references with them
-      negm += tile.y;
-      l *= ex2_approx(tile.y);
-    }
-    uint64_t x[kKeys / 2];     // s - m, in pairs
+    uint64_t y[kKeys / 2];     // y - M, in pairs
     {
-      const uint64_t rw2 = pack2(rw, rw), m2 = pack2(negm, negm);
+      const uint64_t a2 = pack2(a_t, a_t), m2 = pack2(negm + shift, negm + shift);
 #pragma unroll
       for (int ch = 0; ch < kKeys / 32; ++ch) {
         float s[32];
-        tmem_ld32(t_lane + uint32_t(pb) * kKeys + ch * 32, s);
+        tmem_ld32(t_lane + uint32_t(i & 1) * kKeys + ch * 32, s);
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          uint64_t k0, k1;
-          load_pairs(ksc + ch * 32 + k, k0, k1);
-          x[(ch * 32 + k) / 2] = fma2(mul2(pack2(s[k], s[k + 1]), k0), rw2, m2);
-          x[(ch * 32 + k) / 2 + 1] = fma2(mul2(pack2(s[k + 2], s[k + 3]), k1), rw2, m2);
-        }
+        for (int k = 0; k < 32; k += 2) y[(ch * 32 + k) / 2] = fma2(pack2(s[k], s[k + 1]), a2, m2);
       }
       tc_fence_before();
-      mbar_arrive(bar(Cfg::kSEmpty + pb));   // the buffer may take S(i+2)
+      mbar_arrive(bar(Cfg::kSEmpty + (i & 1)));   // the buffer may take S(i+2)
       if (valid < kKeys) {
 #pragma unroll
         for (int k = 0; k < kKeys / 2; ++k) {
-          float x0, x1;
-          unpack2(x[k], x0, x1);
-          x[k] = pack2(2 * k < valid ? x0 : -INFINITY, 2 * k + 1 < valid ? x1 : -INFINITY);
+          float y0, y1;
+          unpack2(y[k], y0, y1);
+          y[k] = pack2(2 * k < valid ? y0 : -INFINITY, 2 * k + 1 < valid ? y1 : -INFINITY);
         }
       }
     }
-    // The largest P (relative to 2^kBias): does the reference have to move?
-    float top = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kKeys; k += 4) {
-      uint64_t e0, e1;
-      float y0, y1, y2, y3;
-      load_pairs(vexp + k, e0, e1);
-      unpack2(add2(x[k / 2], e0), y0, y1);
-      unpack2(add2(x[k / 2 + 1], e1), y2, y3);
-      top = fmaxf(fmaxf(top, y0), y1);
-      top = fmaxf(fmaxf(top, y2), y3);
-    }
+    // P in fp16; again with a moved reference if some row's passed 2^15
+    uint32_t p[kKeys / 2];
+    uint64_t sum2;
     float alpha = 1.f;
-    bool moved = false;
-    if (__any_sync(0xffffffffu, first || top > kLogCodeMax - kBias)) {
-      const float by = first ? top : fmaxf(top, 0.f);
-      const uint64_t b2 = pack2(-by, -by);
+    bool move = first, moved = false;
+    for (;;) {
+      if (move) {
+        float top = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kKeys / 2; ++k) x[k] = add2(x[k], b2);
-      negm -= by;
-      if (!first) {
-        alpha = ex2_approx(-by);
-        l *= alpha;
-        moved = true;
+        for (int k = 0; k < kKeys / 2; ++k) {
+          float y0, y1;
+          unpack2(y[k], y0, y1);
+          top = fmaxf(fmaxf(top, y0), y1);
+        }
+        const float by = first ? top : fmaxf(top, 0.f);
+        const uint64_t b2 = pack2(-by, -by);
+#pragma unroll
+        for (int k = 0; k < kKeys / 2; ++k) y[k] = add2(y[k], b2);
+        negm -= by;
+        if (!first) {
+          alpha = ex2_approx(-by);
+          l *= alpha;
+          moved = true;
+        }
       }
-    }
-    // P in two terms
-    uint32_t hi[kKeys / 4], lo[kKeys / 4];
-    uint64_t sum2 = 0;
+      sum2 = 0;
+      __half2 big = __float2half2_rn(0.f);
 #pragma unroll
-    for (int k4 = 0; k4 < kKeys / 4; ++k4) {
-      uint64_t f[2];
-      load_pairs(vfac + 4 * k4, f[0], f[1]);
-      uint32_t h[2], lw[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float x0, x1, p0, p1;
-        unpack2(x[2 * k4 + j], x0, x1);
-        const uint64_t e = pack2(ex2_approx(x0), ex2_approx(x1));
-        sum2 = add2(sum2, e);
-        unpack2(mul2(e, f[j]), p0, p1);
-        split2_plain(p0, p1, h[j], lw[j]);
+      for (int k = 0; k < kKeys / 2; ++k) {
+        float y0, y1;
+        unpack2(y[k], y0, y1);
+        const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
+        sum2 = add2(sum2, pack2(e0, e1));
+        const __half2 h = __floats2half2_rn(e0, e1);
+        big = __hmax2(big, h);
+        p[k] = *reinterpret_cast<const uint32_t*>(&h);
       }
-      hi[k4] = h[0] | (h[1] << 16);
-      lo[k4] = lw[0] | (lw[1] << 16);
+      const float most = fmaxf(__low2float(big), __high2float(big));
+      if (move || !__any_sync(0xffffffffu, most > kTopP)) break;
+      move = true;
     }
     {
       float s0, s1;
       unpack2(sum2, s0, s1);
-      l += s0 + s1;
+      l = fmaf(s0 + s1, __uint_as_float(uint32_t(127 - rise) << 23), l);
     }
-    // P.V(i-2) must be complete before its P is overwritten, P.V(i-1) before O
-    // is rescaled; a ragged tile needs its V rows landed before those past the
-    // end are zeroed.
-    bool fine = true;
-    if (i > 1) fine = wait(Cfg::kOFull + pb, uint32_t((i >> 1) - 1) & 1);
-    if (i > 0 && moved) fine = wait(Cfg::kOFull + (pb ^ 1), uint32_t((i - 1) >> 1) & 1) && fine;
-    if (valid < kKeys) fine = wait(Cfg::kVFull + st, uint32_t(i / kSV) & 1) && fine;
-    if (!fine) {
+    // P.V(i-1) must be complete before O is rescaled and P overwritten.
+    if (i > 0 && !wait(Cfg::kOFull, uint32_t(i - 1) & 1)) {
       failed = true;
       break;
     }
@@ -428,28 +413,20 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
       }
       tmem_wait_st();
     }
-    unsigned char* const line = lines + pb * Cfg::kPBytes;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      *reinterpret_cast<uint4*>(line + ((j ^ (row & 7)) << 4)) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-      *reinterpret_cast<uint4*>(line + (((4 + j) ^ (row & 7)) << 4)) =
-          make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
-    }
-    if (valid < kKeys) {
-      unsigned char* vst = r.smem + Cfg::kV + st * kTileBytes + valid * 128;
-      for (int k = tid; k < (kKeys - valid) * 8; k += kSoft) *reinterpret_cast<uint4*>(vst + k * 16) = make_uint4(0, 0, 0, 0);
-    }
+    for (int j = 0; j < 8; ++j)
+      *reinterpret_cast<uint4*>(line + ((j ^ (row & 7)) << 4)) = make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
     fence_proxy_async_smem();
     tc_fence_before();
-    mbar_arrive(bar(Cfg::kPFull + pb));
+    mbar_arrive(bar(Cfg::kPFull));
     if (last) {   // the segment's partial; then the next one's queries (its S products wait for them)
-      if (!wait(Cfg::kOFull + pb, uint32_t(i >> 1) & 1)) {
+      if (!wait(Cfg::kOFull, uint32_t(i) & 1)) {
         failed = true;
         break;
       }
       tc_fence_after();
       const int64_t slot = int64_t(blockIdx.x) + seg;
-      const float inv = tile.x * (1.f / (1 << kBias)) * rcp_approx(l);
+      const float inv = scale_of(uint32_t(B0)) * rcp_approx(l);
       float* dst = a.part_o + (slot * kRows + row) * kD;
       const bool mine = int64_t(seg % a.blocks) * kRows + row < rows_all;
 #pragma unroll
@@ -500,14 +477,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int s = 0; s < kSV; ++s) {
       mbar_init(bar(Cfg::kVFull + s), 1);
       mbar_init(bar(Cfg::kVEmpty + s), 1);
-      mbar_init(bar(Cfg::kTabFull + s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(Cfg::kSFull + s), 1);
       mbar_init(bar(Cfg::kSEmpty + s), kSoft);
-      mbar_init(bar(Cfg::kPFull + s), kSoft);
-      mbar_init(bar(Cfg::kOFull + s), 1);
     }
+    mbar_init(bar(Cfg::kPFull), kSoft);
+    mbar_init(bar(Cfg::kOFull), 1);
     mbar_init(bar(Cfg::kQFull), kSoft);
     mbar_init(bar(Cfg::kDone), 2);   // one commit from each issuing thread
     *r.abort = 0;
@@ -527,9 +503,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   // The own rows' kernel may start as this one's CTAs leave room: it reads
   // nothing of this grid's.
   asm volatile("griddepcontrol.launch_dependents;");
-  const int given = __ldg(a.len);
-  r.len = min(max(given, 0), a.m_p);
-  if (r.len != given && blockIdx.x == 0 && threadIdx.x == 0) set_flag(a.flags, MQA_FLAG_LEN_CLAMPED);
+  r.len = min(max(__ldg(a.len), 0), a.m_p);
   r.nb = prefix_tiles(r.len);
   r.t0 = 0;
   r.n = 0;
@@ -546,14 +520,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (r.n > 0) softmax(a, r, warp, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRoles));
-    if (r.n > 0) {
-      if (warp == 2) {
-        v_producer(a, r, &tm_v, lane);
-      } else if (lane == 0) {
-        if (warp == 0) k_producer(a, r, &tm_k);
-        else if (warp == 1) s_issuer(r);
-        else pv_issuer(r);
-      }
+    if (r.n > 0 && lane == 0) {
+      if (warp == 0) producer<true>(a, r, &tm_k);
+      else if (warp == 1) s_issuer(r);
+      else if (warp == 2) producer<false>(a, r, &tm_v);
+      else pv_issuer(r);
     }
     __syncwarp();
   }
@@ -563,10 +534,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (warp == 1) tmem_dealloc(r.tmem, kTmemCols);
 }
 
+// Unpacked rows [g, rows, 128] fp16 as (128, rows, g); a box is 64 columns of
+// 64 rows.
+bool encode_unpacked(CUtensorMap* m, const void* base, int64_t rows, int g) {
+  const cuuint64_t dims[3] = {cuuint64_t(kD), cuuint64_t(rows), cuuint64_t(g)};
+  const cuuint64_t strides[2] = {cuuint64_t(kD) * 2, cuuint64_t(rows) * kD * 2};
+  const cuuint32_t box[3] = {64, kKeys, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
-cudaError_t launch_q8_prefix(const PrefixArgs& a, const uint8_t* k, const uint8_t* v, cudaStream_t stream) {
-  if (int64_t(a.m_p) >= (int64_t(1) << 31) - 512) return cudaErrorInvalidValue;   // row coordinates of a tile
+cudaError_t launch_q8_prefix(const PrefixArgs& a, cudaStream_t stream) {
   static std::atomic<bool> attr_set[64];   // per device; setting it twice is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -578,17 +560,22 @@ cudaError_t launch_q8_prefix(const PrefixArgs& a, const uint8_t* k, const uint8_
   }
   if (encode_fn() == nullptr) return cudaErrorNotSupported;
   CUtensorMap tk, tv;
-  if (!encode_codes(&tk, k, a.m_p, a.g, kKeys) || !encode_codes(&tv, v, a.m_p, a.g, kKeys)) return cudaErrorInvalidValue;
+  if (!encode_unpacked(&tk, a.k16, int64_t(a.tiles) * kKeys, a.g) || !encode_unpacked(&tv, a.v16, int64_t(a.tiles) * kKeys, a.g))
+    return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(a.grid));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg::kAlloc;
+  cfg.gridDim = dim3(unsigned(a.tiles), unsigned(a.g));
+  cfg.blockDim = dim3(kUnpackThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, q8_unpack_kernel, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(unsigned(a.grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg::kAlloc;
   return cudaLaunchKernelEx(&cfg, q8_prefix_tc_kernel, a, tk, tv);
 }
 

@@ -61,19 +61,6 @@ __device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_
   lo = l;
 }
 
-// The same with the second term unscaled (both then go into one accumulator).
-__device__ __forceinline__ void split2_plain(float p0, float p1, uint32_t& hi, uint32_t& lo) {
-  const __half2 p = __floats2half2_rn(p0, p1);
-  uint16_t h, l;
-  uint32_t fu;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(*reinterpret_cast<const uint32_t*>(&p)));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(fu) : "h"(h));
-  const __half2 d = __hsub2(p, *reinterpret_cast<const __half2*>(&fu));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&d)));
-  hi = h;
-  lo = l;
-}
-
 // Sixteen elements of a bf16 query row (zeros when row == nullptr), then as two
 // e4m3 terms of x / s, sixteen codes each; eight neighbouring lanes hold a row
 // (part = lane % 8) and find its power-of-two scale s, which is returned.  x / s reaches (224, 448]; the second term is the rest itself, so
@@ -90,12 +77,12 @@ __device__ __forceinline__ QueryPiece load_query(const __nv_bfloat16* row, int p
   }
   return q;
 }
-__device__ __forceinline__ float split_query(const QueryPiece& q, uint4& hi, uint4& lo) {
-  const uint4(&w)[2] = q.w;
-  float x[16];
+// The piece's values over the row's scale, and the scale; an infinite query
+// gives NaN logits, not saturated ones.
+__device__ __forceinline__ float scale_query(const QueryPiece& q, float (&x)[16]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const uint32_t u = k < 4 ? (&w[0].x)[k] : (&w[1].x)[k - 4];
+    const uint32_t u = k < 4 ? (&q.w[0].x)[k] : (&q.w[1].x)[k - 4];
     const float2 f = bf16x2_to_f32x2(u);
     x[2 * k] = f.x;
     x[2 * k + 1] = f.y;
@@ -107,28 +94,41 @@ __device__ __forceinline__ float split_query(const QueryPiece& q, uint4& hi, uin
   for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const uint32_t e = exponent_for(amax);
   const float inv = inverse_scale(e);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) x[k] = fabsf(x[k]) < INFINITY ? x[k] * inv : NAN;
+  return scale_of(e);
+}
+__device__ __forceinline__ float split_query(const QueryPiece& q, uint4& hi, uint4& lo) {
+  float x[16];
+  const float s = scale_query(q, x);
   uint32_t h[4], l[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     uint32_t h2[2], l2[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float y[2];
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const float v = x[4 * k + 2 * j + z];
-        y[z] = fabsf(v) < INFINITY ? v * inv : NAN;   // an infinite query gives NaN logits, not saturated ones
-      }
-      h2[j] = to_e4m3x2(y[0], y[1]);
+      const float y0 = x[4 * k + 2 * j], y1 = x[4 * k + 2 * j + 1];
+      h2[j] = to_e4m3x2(y0, y1);
       const float2 f = from_e4m3x2(h2[j]);
-      l2[j] = to_e4m3x2(y[0] - f.x, y[1] - f.y);
+      l2[j] = to_e4m3x2(y0 - f.x, y1 - f.y);
     }
     h[k] = h2[0] | (h2[1] << 16);
     l[k] = l2[0] | (l2[1] << 16);
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
-  return scale_of(e);
+  return s;
+}
+// The piece in fp16 over the row's scale, and the scale.
+__device__ __forceinline__ float half_query(const QueryPiece& q, uint32_t (&h)[8]) {
+  float x[16];
+  const float s = scale_query(q, x);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const __half2 t = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
+    h[k] = *reinterpret_cast<const uint32_t*>(&t);
+  }
+  return s;
 }
 
 // ------------------------------------------------------------------ host

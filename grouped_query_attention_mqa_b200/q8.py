@@ -35,7 +35,7 @@ SIGNATURES = {
     "mqa_q8_decode_workspace_size": (_c_size, [_c_int] * 4),
     "mqa_q8_decode": (_c_int, [_c_ptr] * 7 + [_c_int] * 6 + [_c_float, _c_int, _c_ptr, _c_size, _c_ptr,
                                                              ctypes.POINTER(DecodeOptions), _c_ptr]),
-    "mqa_q8_decode_shared_workspace_size": (_c_size, [_c_int] * 4),
+    "mqa_q8_decode_shared_workspace_size": (_c_size, [_c_int] * 5),
     "mqa_q8_decode_shared": (_c_int, [_c_ptr] * 12 + [_c_int] * 6 + [_c_float, _c_int, _c_ptr, _c_size, _c_ptr, _c_ptr]),
 }
 
@@ -275,7 +275,7 @@ class SharedPlan(_Plan):
             out = torch.empty((b, h, d), dtype=q.dtype, device=q.device)
         elif tuple(out.shape) != (b, h, d) or out.dtype != q.dtype:
             raise ValueError("decode_shared: out must be [b, h, d] in q's dtype")
-        ws = _workspace(workspace, int(lib().mqa_q8_decode_shared_workspace_size(b, h, g, d)), q.device)
+        ws = _workspace(workspace, int(lib().mqa_q8_decode_shared_workspace_size(b, h, g, m_p, d)), q.device)
         self.out = out
         self._set("mqa_q8_decode_shared", out, (q, *prefix, prefix_len, *cache, lens, out, ws, status_flags),
                   tuple(_ptr(t) for t in (out, q, *prefix, prefix_len, *cache, lens)) +

@@ -128,14 +128,15 @@ MQA_API mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, 
  *   prefix_len        device int32 [1]  (clamped to [0, m_p])
  *   k/v codes         device [b, m_s, g, d], exponents [b, g, m_s]
  *   lens              device int32 [b]  (clamped to [0, m_s])
- *   workspace         device, mqa_q8_decode_shared_workspace_size(b, h, g, d)
- *                     bytes, as for mqa_q8_decode
+ *   workspace         device, mqa_q8_decode_shared_workspace_size(b, h, g,
+ *                     m_p, d) bytes, as for mqa_q8_decode; among it the prefix
+ *                     in fp16, unpacked anew by every call
  *
  * MQA_FLAG_LEN_CLAMPED reports lengths outside [0, m]; 0 is a length here.
  * A sequence with no rows at all gets a zero row.  Built for bf16, d = 128
  * and h/g <= 64 (MQA_ERR_UNSUPPORTED otherwise).
  */
-MQA_API size_t mqa_q8_decode_shared_workspace_size(int b, int h, int g, int d);
+MQA_API size_t mqa_q8_decode_shared_workspace_size(int b, int h, int g, int m_p, int d);
 MQA_API mqa_status_t mqa_q8_decode_shared(void* o, const void* q, const void* prefix_k, const uint8_t* prefix_k_exps,
                                           const void* prefix_v, const uint8_t* prefix_v_exps,
                                           const int32_t* prefix_len, const void* k_codes, const uint8_t* k_exps,

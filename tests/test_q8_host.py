@@ -165,12 +165,13 @@ def test_shared_refusals(lib):
     for name in ("o", "q", "pk", "pv", "pl", "k", "v", "lens", "ws"):
         assert _shared(lib, **{name: ODD}) == INV
     size = lib.mqa_q8_decode_shared_workspace_size
-    assert _shared(lib, ws_bytes=size(2, 8, 1, 128) - 1) == INV
+    assert _shared(lib, ws_bytes=size(2, 8, 1, 64, 128) - 1) == INV
     assert _shared(lib, g=3) == INV and _shared(lib, m_p=0) == INV and _shared(lib, m_s=0) == INV and _shared(lib, b=-1) == INV
     assert _shared(lib, scale=float("inf")) == INV and _shared(lib, dtype=9) == INV
     assert _shared(lib, dtype=binding.MQA_F32) == UNS and _shared(lib, d=64) == UNS and _shared(lib, h=65) == UNS
     assert _shared(lib, b=0) == OK
-    assert size(2, 8, 3, 128) == 0 and size(2, 65, 1, 128) == 0 and size(0, 8, 1, 128) > 0
+    assert size(2, 8, 3, 64, 128) == 0 and size(2, 65, 1, 64, 128) == 0 and size(2, 8, 1, 0, 128) == 0
+    assert size(0, 8, 1, 64, 128) > 0
 
 
 def test_binding_refuses_other_layouts():
