@@ -888,9 +888,9 @@ __global__ void __launch_bounds__(Cfg<HP>::kThreads, kCtasPerSm)
   // The barriers are initialised before the schedule starts loads on them.
   __syncthreads();
   // Inputs may come from the kernel before this one on the stream (the append).
-  // Beside a prefix kernel nothing is read that it writes, and it has let this
-  // grid start only after its own wait for what came before: that wait stands
-  // for this one's, which comes at the end, for the merge.
+  // Beside a shared prefix nothing is read that its kernels write, and the first
+  // of them has let the others start only after its wait for what came before:
+  // that wait stands for this one's, which comes at the end, for the merge.
   if (!a.partials) asm volatile("griddepcontrol.wait;" ::: "memory");
   int* lens_tab = reinterpret_cast<int*>(r.smem + C::kLens);
   r.lens_s = lens_tab;

@@ -191,6 +191,7 @@ __device__ void producer(const PrefixArgs& a, const Roles& r, const CUtensorMap*
   auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };
   uint64_t pol;   // the tiles are read again by the other blocks
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the unpacked tiles
   Walk w(r);
   int i = 0;
   for (; i < r.n; ++i) {
@@ -302,8 +303,9 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
   };
 
   w.next();
-  int2 exps = a.tile_exps[w.seg / a.blocks * a.tiles + w.k];   // the next tile's A and B
   convert(w.seg);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the unpacked tiles, from here on
+  int2 exps = a.tile_exps[w.seg / a.blocks * a.tiles + w.k];   // the next tile's A and B
   float negm = 0.f, l = 0.f, rw = 0.f;   // minus the row's reference, its sum, its query scale
   int B0 = 119;
   bool failed = !query_scale(0, rw);
@@ -499,9 +501,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   __syncthreads();
   tc_fence_after();
   r.tmem = *reinterpret_cast<volatile uint32_t*>(r.smem + Cfg::kTmemSlot);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // The own rows' kernel may start as this one's CTAs leave room: it reads
-  // nothing of this grid's.
+  // The own rows' kernel may start wherever this one leaves room: it reads
+  // nothing of this grid's or of the unpacking's, and what came before them is
+  // complete (the unpacking let this grid start after its own wait).
   asm volatile("griddepcontrol.launch_dependents;");
   r.len = min(max(__ldg(a.len), 0), a.m_p);
   r.nb = prefix_tiles(r.len);
