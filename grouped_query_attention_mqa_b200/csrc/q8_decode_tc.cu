@@ -17,11 +17,11 @@
 //   S^T[t, i]  = k_t . (q1_i + q2_i)    M = 128 rows, N = heads, K = 2 x 128
 //   s_{t,i}    = scale log2(e) w_i a_t S[t, i]
 //   p_{t,i}    = 2^(s_{t,i} - m_i),     l_i = sum_t p_{t,i}            (fp32)
-//   P_{t,i}    = p_{t,i} b_t 2^(3-E)
+//   P_{t,i}    = p_{t,i} b_t 2^(2-E)
 //   O^T[c, n] += sum_t v_t[c] P[t, n]   M = 128 columns of V, N = 2 heads, K = 128 rows
-//   o_i        = 2^(E-3) (O[c, i] + O[c, i'] / 16) / l_i
+//   o_i        = 2^(E-2) (O[c, i] + O[c, i'] / 16) / l_i
 // E is the largest value-row exponent seen (of rows that are not all zero) and
-// m_i is set so that the largest P is 2^3: the e4m3 grid (at least 2^-13 in the
+// m_i is set so that the largest P is 2^2: the e4m3 grid (at least 2^-13 in the
 // second term) then lies relative to what a row contributes to the output, not
 // to its weight alone, and a heavy row with small values (an attention sink)
 // leaves the other rows their precision.  A reference is moved only when some P
@@ -60,8 +60,8 @@ constexpr int kRows = 128;                      // rows per tile: the products' 
 constexpr int kKWarp = 0, kSWarp = 1, kVWarp = 2, kSoftWarp = 4;   // warp 3: P.V products
 constexpr int kCtasPerSm = 2;
 constexpr uint32_t kTileBytes = kRows * kD;     // 128 rows of codes, 128-byte swizzled
-constexpr int kSegUnits = 4;                    // cost of entering a segment, in quarter tiles
-constexpr int kBias = 3;                        // the largest P after a reference is set is 2^kBias
+constexpr int kSegUnits = 7;                    // cost of entering a segment, in quarter tiles (measured: 2.7 us, a tile 1.6)
+constexpr int kBias = 2;                        // the largest P after a reference is set is 2^kBias
 constexpr int kLensCache = 256;
 constexpr uint32_t kMaxDynSmem = (233472 - kCtasPerSm * 1024) / kCtasPerSm;
 
@@ -220,7 +220,10 @@ __device__ Run make_run(const TcArgs& a, int group, bool report, int64_t* scratc
   const int excl_t = int(incl >> 32) - my_t, excl_u = int(uint32_t(incl)) - my_u;
   Run run = {};
   run.wtotal = W;
-  const int cap = W / (kSegUnits + 4);   // every range then holds a tile's start
+  // Ranges of four units and more: a range that starts and ends within one
+  // sequence then holds a tile's start, so that the parts of a segment lie in
+  // consecutive groups; a range may be empty where it covers a segment's entry.
+  const int cap = W / 4;
   run.active = cap < a.groups ? cap : a.groups;
   if (group >= run.active) return run;   // uniform across the CTA
   const int q = W / run.active, rm = W - q * run.active;   // group*W/active without a 64-bit division
