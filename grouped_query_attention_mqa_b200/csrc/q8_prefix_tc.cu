@@ -193,16 +193,17 @@ __device__ void producer(const PrefixArgs& a, const Roles& r, const CUtensorMap*
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the unpacked tiles
   Walk w(r);
-  int i = 0;
+  int i = 0, head = 0;
   for (; i < r.n; ++i) {
     w.next();
     if (*r.abort) break;
     const int st = i % S;
     if (i >= S && !wait_bar(r, bar(kEmpty + st), uint32_t(i / S - 1) & 1)) break;
     const uint32_t dst = r.sbase + kRing + st * kTileBytes;
+    if (w.first) head = w.seg / a.blocks;
     mbar_expect_tx(bar(kFull + st), kTileBytes);
-    tma_load_3d(dst, map, bar(kFull + st), 0, w.k * kKeys, w.seg / a.blocks, pol);
-    tma_load_3d(dst + kHalf, map, bar(kFull + st), 64, w.k * kKeys, w.seg / a.blocks, pol);
+    tma_load_3d(dst, map, bar(kFull + st), 0, w.k * kKeys, head, pol);
+    tma_load_3d(dst + kHalf, map, bar(kFull + st), 64, w.k * kKeys, head, pol);
   }
   // every copy issued has landed before the CTA can exit
   for (int j = (i - S > 0 ? i - S : 0); j < i; ++j) mbar_wait_asleep(bar(kFull + j % S), uint32_t(j / S) & 1, kTimeoutNs);
@@ -305,7 +306,8 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
   w.next();
   convert(w.seg);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the unpacked tiles, from here on
-  int2 exps = a.tile_exps[w.seg / a.blocks * a.tiles + w.k];   // the next tile's A and B
+  const int2* tile_exps = a.tile_exps + w.seg / a.blocks * a.tiles;
+  int2 exps = tile_exps[w.k];   // the next tile's A and B
   float negm = 0.f, l = 0.f, rw = 0.f;   // minus the row's reference, its sum, its query scale
   int B0 = 119;
   bool failed = !query_scale(0, rw);
@@ -316,7 +318,8 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
     const int2 e = exps;
     if (i + 1 < r.n) {
       w.next();
-      exps = a.tile_exps[w.seg / a.blocks * a.tiles + w.k];
+      if (w.first) tile_exps = a.tile_exps + w.seg / a.blocks * a.tiles;
+      exps = tile_exps[w.k];
     }
     const bool last = i + 1 == r.n || w.first;
     if (first) {
@@ -429,19 +432,27 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
       tc_fence_after();
       const int64_t slot = int64_t(blockIdx.x) + seg;
       const float inv = scale_of(uint32_t(B0)) * rcp_approx(l);
-      float* dst = a.part_o + (slot * kRows + row) * kD;
-      const bool mine = int64_t(seg % a.blocks) * kRows + row < rows_all;
+      // 32 columns at a time through the warp's own lines of P, so that whole
+      // 128-byte lines leave the SM (a row per lane, 32 bytes each, took four
+      // times the requests: 5.5 us at the end of every CTA).
+      const int rows_left = int(min(int64_t(kRows), rows_all - int64_t(seg % a.blocks) * kRows)) - 32 * q4;   // of this warp's 32
+      const bool mine = lane < rows_left;
+      float4* const box = reinterpret_cast<float4*>(r.smem + Cfg::kP + q4 * 4096);   // [32 rows][8 pieces], swizzled
+      float* const dst = a.part_o + (slot * kRows + 32 * q4) * kD;
 #pragma unroll
       for (int ch = 0; ch < kD / 32; ++ch) {
         float v[32];
         tmem_ld32(t_lane + kOCol + ch * 32, v);
-        if (mine) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)   // 32 bytes per lane: whole sectors
-            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + ch * 32 + k), "f"(v[k] * inv),
-                         "f"(v[k + 1] * inv), "f"(v[k + 2] * inv), "f"(v[k + 3] * inv), "f"(v[k + 4] * inv),
-                         "f"(v[k + 5] * inv), "f"(v[k + 6] * inv), "f"(v[k + 7] * inv) : "memory");
+        for (int k = 0; k < 8; ++k)
+          box[lane * 8 + (k ^ (lane & 7))] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rr = 4 * k + lane / 8, piece = lane % 8;
+          if (rr < rows_left) *reinterpret_cast<float4*>(dst + rr * kD + ch * 32 + piece * 4) = box[rr * 8 + (piece ^ (rr & 7))];
         }
+        __syncwarp();
       }
       if (mine) a.part_lse[slot * kRows + row] = lg2_approx(l) - negm;
       tc_fence_before();   // O has been read before the next P is announced
