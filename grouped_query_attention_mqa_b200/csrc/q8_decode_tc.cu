@@ -174,7 +174,7 @@ struct Run {
 // Clamped rows of sequence s.  Where another part joins the partials a
 // sequence may have none of its own.
 __device__ __forceinline__ int rows_of(const TcArgs& a, int s, bool report) {
-  const int n = __ldg(a.lens + s), c = min(max(n, 0), a.m);
+  const int n = __ldcg(a.lens + s), c = min(max(n, 0), a.m);
   if (report && (c != n || (n == 0 && !a.partials))) set_flag(a.flags, MQA_FLAG_LEN_CLAMPED);
   return c;
 }
@@ -535,8 +535,8 @@ __device__ void softmax_epilogue(const TcArgs& a, const Run& run, const Roles& r
       ve += kRows;
     }
     const bool in = w.row0 + row < w.len;
-    nke = in ? *ke : 0u;
-    nve = in ? *ve : 0u;
+    nke = in ? __ldcg(ke) : 0u;
+    nve = in ? __ldcg(ve) : 0u;
   };
   w.next(a, r);
   load_exps();
@@ -894,6 +894,7 @@ __global__ void __launch_bounds__(Cfg<HP>::kThreads, kCtasPerSm)
   // Beside a shared prefix nothing is read that its kernels write, and the first
   // of them has let the others start only after its wait for what came before:
   // that wait stands for this one's, which comes at the end, for the merge.
+  // (Inputs are read past the L1, which nothing has cleaned for this grid then.)
   if (!a.partials) asm volatile("griddepcontrol.wait;" ::: "memory");
   int* lens_tab = reinterpret_cast<int*>(r.smem + C::kLens);
   r.lens_s = lens_tab;

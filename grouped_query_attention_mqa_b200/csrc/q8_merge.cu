@@ -32,11 +32,11 @@ __global__ void __launch_bounds__(kThreads) q8_merge_kernel(const TcArgs a, cons
   const int s = active ? int(item / unsigned(a.h)) : 0, head = active ? int(item - unsigned(s) * a.h) : 0;
   const int j = head / a.hq, i = head - j * a.hq;
   // The lengths are inputs, not written by the kernels this one follows.
-  const bool has_own = __ldg(a.lens + s) > 0;
+  const bool has_own = __ldcg(a.lens + s) > 0;
   int pre_n = 0;                    // parts of the row's prefix segment
   int64_t pre_at = 0;               // the first of them, then one every kPrefixRows
   if (prefix) {
-    const int nb = prefix_tiles(min(max(__ldg(p.len), 0), p.m_p));
+    const int nb = prefix_tiles(min(max(__ldcg(p.len), 0), p.m_p));
     const unsigned row = unsigned(s) * unsigned(a.hq) + unsigned(i);
     const int seg = j * p.blocks + int(row / kPrefixRows);
     if (nb > 0) {

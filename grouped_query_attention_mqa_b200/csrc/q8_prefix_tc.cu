@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   // nothing of this grid's or of the unpacking's, and what came before them is
   // complete (the unpacking let this grid start after its own wait).
   asm volatile("griddepcontrol.launch_dependents;");
-  r.len = min(max(__ldg(a.len), 0), a.m_p);
+  r.len = min(max(__ldcg(a.len), 0), a.m_p);
   r.nb = prefix_tiles(r.len);
   r.t0 = 0;
   r.n = 0;

@@ -72,8 +72,8 @@ struct QueryPiece {
 __device__ __forceinline__ QueryPiece load_query(const __nv_bfloat16* row, int part) {
   QueryPiece q = {};
   if (row != nullptr) {
-    q.w[0] = *reinterpret_cast<const uint4*>(row + part * 16);
-    q.w[1] = *reinterpret_cast<const uint4*>(row + part * 16 + 8);
+    q.w[0] = __ldcg(reinterpret_cast<const uint4*>(row + part * 16));
+    q.w[1] = __ldcg(reinterpret_cast<const uint4*>(row + part * 16 + 8));
   }
   return q;
 }

@@ -118,9 +118,28 @@ def _same_device(first, *others):
             raise ValueError("libmqa needs all tensors of a call on one device")
 
 
+def _on(stream):
+    """Allocations made here belong to the stream that will use them: memory
+    freed with a plan is then reused in that stream's order."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _workspace(workspace, need, device, stream):
+    import torch
+    if workspace is None:
+        with _on(stream):
+            return torch.empty(max(256, need), dtype=torch.uint8, device=device)
+    return workspace
+
+
 class _Plan:
     """One C call with its arguments marshalled; tensors it points to are kept.
     ``stream`` None is the current stream of the tensors' device at each run.
+    Like any tensor in use, a plan is kept until the work of its runs is done
+    (and while a graph that captured a run may still be replayed); runs of one
+    plan must be ordered on the GPU, as they share its workspace.
 
     The arguments are ctypes objects made once and handed to a function object
     without declared argument types, which skips their conversion at every call
@@ -193,7 +212,8 @@ class ReadPlan(_Plan):
             raise ValueError("read: total must not be negative")
         if out is None:
             dtype = torch.bfloat16 if dtype is None else dtype
-            out = tuple(torch.zeros((total, g, d), dtype=dtype, device=cache.k.device) for d in (d_k, d_v))
+            with _on(stream):
+                out = tuple(torch.zeros((total, g, d), dtype=dtype, device=cache.k.device) for d in (d_k, d_v))
         k_out, v_out = out
         _check_cuda(cu_rows, start, k_out, v_out, status_flags)
         _same_device(cache.k, *cache[1:], cu_rows, start, k_out, v_out, status_flags)
@@ -211,13 +231,6 @@ class ReadPlan(_Plan):
 
 def decode_workspace_size(b, h, g, d_v):
     return int(lib().mqa_q8_decode_workspace_size(b, h, g, d_v))
-
-
-def _workspace(workspace, need, device):
-    import torch
-    if workspace is None:
-        return torch.empty(max(256, need), dtype=torch.uint8, device=device)
-    return workspace
 
 
 class DecodePlan(_Plan):
@@ -238,10 +251,11 @@ class DecodePlan(_Plan):
         h = q.shape[1]
         _check_i32(lens, b, "lens")
         if out is None:
-            out = torch.empty((b, h, d_v), dtype=q.dtype, device=q.device)
+            with _on(stream):
+                out = torch.empty((b, h, d_v), dtype=q.dtype, device=q.device)
         elif tuple(out.shape) != (b, h, d_v) or out.dtype != q.dtype:
             raise ValueError("decode: out must be [b, h, d_v] in q's dtype")
-        ws = _workspace(workspace, decode_workspace_size(b, h, g, d_v), q.device)
+        ws = _workspace(workspace, decode_workspace_size(b, h, g, d_v), q.device, stream)
         self.out = out
         self._opts = DecodeOptions(PATHS[path], int(num_ctas), int(window))
         self._set("mqa_q8_decode", out, (q, *cache, lens, out, ws, status_flags),
@@ -272,10 +286,11 @@ class SharedPlan(_Plan):
         _check_i32(prefix_len, 1, "prefix_len")
         _check_i32(lens, b, "lens")
         if out is None:
-            out = torch.empty((b, h, d), dtype=q.dtype, device=q.device)
+            with _on(stream):
+                out = torch.empty((b, h, d), dtype=q.dtype, device=q.device)
         elif tuple(out.shape) != (b, h, d) or out.dtype != q.dtype:
             raise ValueError("decode_shared: out must be [b, h, d] in q's dtype")
-        ws = _workspace(workspace, int(lib().mqa_q8_decode_shared_workspace_size(b, h, g, m_p, d)), q.device)
+        ws = _workspace(workspace, int(lib().mqa_q8_decode_shared_workspace_size(b, h, g, m_p, d)), q.device, stream)
         self.out = out
         self._set("mqa_q8_decode_shared", out, (q, *prefix, prefix_len, *cache, lens, out, ws, status_flags),
                   tuple(_ptr(t) for t in (out, q, *prefix, prefix_len, *cache, lens)) +

@@ -241,3 +241,42 @@ def test_two_captured_calls_do_not_share_a_workspace():
     torch.cuda.synchronize()
     for p, (ref, tol) in zip(plans, want):
         assert_within(p.out, ref, tol)
+
+
+def test_calls_on_a_given_stream():
+    """Functions (not plans) on a side stream, back to back, with the caller's
+    stream busy allocating: each call's workspace belongs to the side stream."""
+    rng = np.random.default_rng(15)
+    arrays = host_cache(rng, 2, 1200, 2, 128)
+    lens = [1200, 700]
+    qs = [round_to(rng.standard_normal((2, 32, 128)), "bf16") for _ in range(4)]
+    want = [attention(q64, cache_parts(arrays, lens), 2, 0.1, "bf16", two_terms=True) for _, q64 in qs]
+    cache, lens_d, qd = dev_cache(arrays), i32(lens), [q.cuda() for q, _ in qs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = []
+    for q in qd * 5:
+        outs.append(q8.decode(q, cache, lens_d, 0.1, stream=side))
+        torch.empty(64 << 20, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    for k, o in enumerate(outs):
+        assert_within(o, *want[k % 4])
+
+
+def test_refusals_raise():
+    cache = q8.new_cache(2, 8, 1, 128)
+    q = torch.zeros((2, 4, 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(binding.MqaError, match="UNSUPPORTED"):
+        q8.decode(q.float(), cache, i32([1, 1]), 1.0, path="tcgen05")
+    with pytest.raises(binding.MqaError, match="INVALID_ARG"):
+        q8.decode(q, cache, i32([1, 1]), float("nan"))
+    with pytest.raises(ValueError):
+        q8.decode(q[:1], cache, i32([1, 1]), 1.0)
+    with pytest.raises(TypeError):
+        q8.decode(q, (cache.k.view(torch.uint8), *cache[1:]), i32([1, 1]), 1.0)
+    with pytest.raises(ValueError):
+        q8.decode(q, cache, i32([1, 1]).long(), 1.0)
+    with pytest.raises(ValueError):
+        q8.append(cache, q[:1, :1], q[:1, :1], i32([0, 0]))
+    empty = q8.new_cache(0, 8, 1, 128)
+    assert q8.decode(q[:0], empty, i32([]), 1.0).shape == (0, 4, 128)
