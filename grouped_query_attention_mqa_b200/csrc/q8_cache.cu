@@ -6,13 +6,15 @@
 // power of two with amax <= 448 s, code = e4m3(x / s).  The division is a
 // multiplication by an exact power of two, so the only rounding is the one to
 // e4m3.  Bound: HBM (2 or 4 bytes read and one written per element; the read
-// the other way round); a decode step's few rows are bound by the launch.
+// the other way round): eight bf16 prompts of up to 4,096 rows with 8 heads of
+// 128, 118 MB, are written in 20.8 us, 16 of them, 252 MB, read back in 41.7 us
+// (5.7 and 6.0 TB/s).  A decode step's few rows are bound by the launch (1.7 us).
 //
 // Both kernels give every thread 16 elements (32-byte loads and stores of bf16,
 // 16-byte ones of codes), so d / 16 neighbouring lanes hold a row and find its
-// maximum with shuffles: each byte is read once, in one pass.  A block takes `rows` consecutive packed rows of all heads, which are
-// contiguous in the packed array, and looks their sequences up once for all
-// heads.
+// maximum with shuffles: each byte is read once, in one pass.  A block takes
+// `rows` consecutive packed rows of all heads, which are contiguous in the
+// packed array, and looks their sequences up once for all heads.
 #include "q8.cuh"
 
 namespace mqa {

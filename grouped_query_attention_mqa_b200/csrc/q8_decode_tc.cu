@@ -25,15 +25,18 @@
 // second term) then lies relative to what a row contributes to the output, not
 // to its weight alone, and a heavy row with small values (an attention sink)
 // leaves the other rows their precision.  A reference is moved only when some P
-// would pass 448.
+// would pass 448.  Behind a heavy row a long tail's weights can all be below
+// that grid: they are dithered before they are rounded, so that their sum stays
+// (lowering a reference with a tile's maxima instead cost 24% on 32K-row GQA-8
+// caches whose row scales vary: it goes up and down all the time).
 //
 // Work: two persistent CTAs per SM (a tile's chain of product, softmax and
 // product is latency; two chains hide each other's).  CTA c serves K/V head c %
 // g over a contiguous run of all sequences' 128-row tiles, balanced in quarter
 // tiles with a segment's entry weighed as a whole tile.  The g CTAs of a group
 // walk the same rows in step: a cache row's g heads are neighbours in memory,
-// 128 bytes each, and reading them together is what DRAM pages want (GQA-8
-// with 32K-row caches: 287 us head by head, see the table of measurements).
+// 128 bytes each, and reading them together is what DRAM pages want (32 GQA-8
+// caches of 8K to 32K rows, 1.44 GB: 287 us head by head, 237 in step).
 // Partials of split segments are joined by the merge kernel.  Roles:
 //   warp 0, lane 0    K loads;      warp 2, lane 0   V loads (never ahead of K)
 //   warp 1, lane 0    S products;   warp 3, lane 0   P.V products
@@ -44,9 +47,10 @@
 // expiry the kernel sets MQA_FLAG_PIPE_TIMEOUT, drains its copies and products,
 // frees its tensor memory and returns.
 //
-// Bound: HBM for large caches and groups of up to 16 heads (d + 1 bytes per row
-// instead of 2 d); the chain's latency for wider groups; the fixed costs of a
-// launch for small caches.
+// Bound: HBM for large caches and groups of up to 16 heads (those 1.44 GB: 223
+// us, 6.4 TB/s, where the clocks are good; d + 1 bytes per row instead of 2 d);
+// the chain's latency for wider groups (64 MQA caches of 1K to 8K rows with 32
+// heads, 80 MB: 33 us, 2.4 TB/s); the fixed costs of a launch for small caches.
 #include "q8_tc.cuh"
 
 namespace mqa {
@@ -585,6 +589,7 @@ __device__ void softmax_epilogue(const TcArgs& a, const Run& run, const Roles& r
   for (int i = 0; i < n; ++i) {
     const float kr = scale_of(nke) * c;
     const int er = int(nve);
+    const __half2 dither = row_dither(w.row0 + row);
     const int rows = w.rows(), sidx = w.sidx;
     const bool first = w.first, last = w.last();
     if (last && tid == 0) {   // what the epilogue will need
@@ -746,7 +751,7 @@ __device__ void softmax_epilogue(const TcArgs& a, const Run& run, const Roles& r
             ls = add2(ls, e);
             float p0, p1;
             unpack2(mul2(e, ab2), p0, p1);
-            split2(p0, p1, h[j], l[j]);
+            split2(p0, p1, dither, h[j], l[j]);
           }
           hi[ch * (W / 4) + k4] = h[0] | (h[1] << 16);
           lo[ch * (W / 4) + k4] = l[0] | (l[1] << 16);

@@ -6,10 +6,10 @@
 // Two kernels.  The first unpacks the prefix to fp16, once for the whole batch:
 // tile by tile of 64 rows, each tile relative to its largest key and its largest
 // value exponent,
-//   k'_t = code_t 2^(a_t - A),   v'_t = code_t 2^(b_t - B)      (exact: a code has 4 bits; rows
-// 2^-15 and more below their tile's largest lose bits below 2^-24 of a unit of
-// which that has 224), zeros past the prefix's end.  The second is a
-// flash-style product over query blocks: the rows of one K/V head are the pairs
+//   k'_t = code_t 2^(a_t - A),   v'_t = code_t 2^(b_t - B)      (exact, a code has 4 bits; rows
+// 2^-9 and more below their tile's largest scale lose what is below 2^-25 of a
+// unit of which that row has up to 448), zeros past the prefix's end.  The
+// second is a product with a running softmax over query blocks: the rows of one K/V head are the pairs
 // (sequence, head of the group), in that order, and with x_r = q_r / w_r in
 // fp16 (maximum in (224, 448], bf16's 8 bits exact to 2^-17 of a unit)
 //   S[r, t]  = x_r . k'_t              M = 128 query rows, N = 64 keys, K = 128
@@ -20,11 +20,17 @@
 //   o_r      = 2^B_0 O[r, :] / l_r
 // B_0 is the first tile's B: the value exponent enters with the logit, so that a
 // reference M_r is the largest contribution to the output, not the largest
-// weight.  fp16 spans 40 octaves: P starts at 1, a reference moves only when
-// some P would pass 2^15, and what is below 2^-24 of the reference is dropped.
+// weight.  fp16 spans 40 octaves: P starts at 2^2, a reference moves only when
+// some P would pass 2^15, and weights round to steps of 2^-24, 2^-26 of the
+// reference's: 2^18 rows that all lose half a step lose 2^-9 of it.  (Started at
+// 2^0: 186 us instead of 190 for 128 sequences behind a 16K prefix with GQA-8
+// and row scales that vary; at 2^4 195, at 2^8 228: the references move more
+// often.)
 // (The same product on the e4m3 codes as they are, with both operands in two
-// e4m3 terms and per-row scale tables, took 1.9 times as long: the softmax
-// threads' instructions bound it, and a reference moved every third tile.)
+// e4m3 terms and per-row scale tables: 158 us instead of 116 for that prefix,
+// the softmax threads' instructions, with a reference moving every third tile;
+// exponents of single rows brought to P where a tile's values are far apart: 10%
+// more for every call.)
 // Here query rows are the products' M, so that a row's softmax is one thread's
 // own: no barrier and no reduction across threads.
 //
@@ -36,7 +42,9 @@
 // each), warps 4-7 queries, softmax and output, a row per thread.  Every wait is
 // bounded (one second) and reported with MQA_FLAG_PIPE_TIMEOUT.
 //
-// Bound: the softmax threads' instructions and latency.
+// Bound: the softmax threads' instructions and latency (that prefix: 67 GFLOP
+// and 131 million exponentials in 116 us, 0.58 PFLOP/s; their floors are 41 and
+// 29 us).
 #include "q8_tc.cuh"
 
 namespace mqa {
@@ -51,6 +59,7 @@ constexpr int kThreads = 256, kSoft = 128, kSoftWarp = 4;
 constexpr int kCtasPerSm = 2;
 constexpr int kRegsRoles = 72, kRegsSoft = 184;   // of the 128 per thread at launch
 constexpr float kTopP = 32768.f;                  // P stays below it: half of fp16's range
+constexpr int kBias = 2;                          // the largest P after a reference is set is 2^kBias
 constexpr int kSK = 2, kSV = 2;                   // ring stages
 constexpr uint32_t kQHalf = kRows * 128, kHalf = kKeys * 128;   // 64 columns: 128-byte swizzled rows
 constexpr uint32_t kTileBytes = 2 * kHalf;
@@ -369,7 +378,7 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
           unpack2(y[k], y0, y1);
           top = fmaxf(fmaxf(top, y0), y1);
         }
-        const float by = first ? top : fmaxf(top, 0.f);
+        const float by = first ? top - float(kBias) : fmaxf(top - float(kBias), 0.f);
         const uint64_t b2 = pack2(-by, -by);
 #pragma unroll
         for (int k = 0; k < kKeys / 2; ++k) y[k] = add2(y[k], b2);

@@ -46,8 +46,10 @@ __device__ __forceinline__ void load_pairs(const float* p, uint64_t& a, uint64_t
 }
 
 // Two weights -> their two e4m3 terms (two codes each).  The difference is
-// taken in fp16: its 11 bits hold what the second term's 4 can use.
-__device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+// taken in fp16: its 11 bits hold what the second term's 4 can use.  `dither`,
+// within half of e4m3's smallest step (2^-9), is added to the second term, in
+// both halves: see row_dither.
+__device__ __forceinline__ void split2(float p0, float p1, __half2 dither, uint32_t& hi, uint32_t& lo) {
   const __half2 p = __floats2half2_rn(p0, p1);
   const uint32_t pu = *reinterpret_cast<const uint32_t*>(&p);
   uint16_t h, l;
@@ -55,10 +57,20 @@ __device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(pu));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(fu) : "h"(h));
   const __half2 f = *reinterpret_cast<const __half2*>(&fu);
-  const __half2 d = __hmul2(__hsub2(p, f), __float2half2_rn(16.f));
+  const __half2 d = __hfma2(__hsub2(p, f), __float2half2_rn(16.f), dither);
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&d)));
   hi = h;
   lo = l;
+}
+
+// What cache row t adds to its weights before they are rounded: one of 256
+// values evenly spread over a step of e4m3's smallest, neighbouring rows' far
+// apart (multiples of the golden ratio).  A weight far below a step then becomes
+// a step as often as its size says, so that thousands of rows that are each
+// lost in the grid behind one heavy row still add up to what they weigh; a
+// weight of 0 stays 0.
+__device__ __forceinline__ __half2 row_dither(int t) {
+  return __float2half2_rn((float((uint32_t(t) * 2654435769u) >> 24) - 127.5f) * (1.f / 131072));
 }
 
 // Sixteen elements of a bf16 query row (zeros when row == nullptr), then as two

@@ -17,17 +17,17 @@
  *   exponents  device uint8 [b, g, m_max]
  *
  * The library writes E in [1, 254]; rows that are attended to must not hold
- * E = 255.  A power of two costs e4m3 no precision
- * (it is a floating format), makes code * s exact in bf16 and fp32, and makes
- * quantising what was read back give the same codes and exponent again.  The
- * exponents of one head lie in row order, so a tile's are one short run.
+ * E = 255.  A power of two costs e4m3 no precision (it is a floating format),
+ * makes code * s exact in bf16 and fp32, and makes quantising what was read
+ * back give the same codes and exponent again.  The exponents of one head lie in
+ * row order, so a tile's are one short run.
  *
  * Conventions are those of mqa.h: caller-owned device pointers on the current
  * device, 16-byte aligned except the exponent arrays (any alignment) and the
- * packed rows of mqa_q8_append and mqa_q8_read (32-byte aligned), not aliased; dense row-major tensors; asynchronous on `stream`; arguments
- * checked before any launch; no allocation, no state between calls, no
- * exceptions; device-read values are clamped or skipped and reported in
- * *status_flags (NULL to ignore).
+ * packed rows of mqa_q8_append and mqa_q8_read (32-byte aligned), not aliased;
+ * dense row-major tensors; asynchronous on `stream`; arguments checked before
+ * any launch; no allocation, no state between calls, no exceptions; device-read
+ * values are clamped or skipped and reported in *status_flags (NULL to ignore).
  */
 #ifndef LIBMQA_MQA_Q8_H
 #define LIBMQA_MQA_Q8_H
@@ -99,7 +99,11 @@ MQA_API mqa_status_t mqa_q8_read(void* k_out, void* v_out, const void* k_codes, 
  *   opts     path, CTA count and local window, as for mqa_decode_ex, or NULL
  *
  * Rows at or past lens[b], and rows before the window, never count, whatever
- * codes and exponents they hold.  Statistics and sums are fp32.
+ * codes and exponents they hold.  Statistics and sums are fp32.  On the
+ * tensor-core path a row's weight is rounded to 2^-9 of itself, or to steps of
+ * 2^-15 of the largest p_t s_t (weight times value scale) where that is more,
+ * up or down as often as its size says; a query's elements to 2^-17 of its
+ * largest.
  * Paths: the tensor-core path takes bf16 with d_k = d_v = 128 and h/g <= 64,
  * and is then the automatic choice; the CUDA-core path takes both types with
  * d_k, d_v in {32, 64, 128} and h/g * d_k, h/g * d_v <= 4096.
@@ -133,6 +137,10 @@ MQA_API mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, 
  *                     in fp16, unpacked anew by every call
  *
  * MQA_FLAG_LEN_CLAMPED reports lengths outside [0, m]; 0 is a length here.
+ * The prefix's values count with 2^-25 of the largest value scale among the 64
+ * rows from a multiple of 64 on, their weights with 2^-12 of themselves or 2^-27
+ * of the largest p_t s_t, s_t that largest scale; such scales of one K/V head
+ * are at most 2^126 apart.  The own rows are taken as by mqa_q8_decode.
  * A sequence with no rows at all gets a zero row.  Built for bf16, d = 128
  * and h/g <= 64 (MQA_ERR_UNSUPPORTED otherwise).
  */

@@ -12,9 +12,10 @@ output computed with |V|; L the largest sum of |q_c k_c| * |scale|):
    |scale|, a weight relatively by twice that (M its largest value):
        A 2 (2^-10 / 224) M;
    a weight to two e4m3 terms, at most 2^-9 of it, and the smallest weights to
-   a grid: either steps of 2^-13 where the largest p_t s_t (s_t the value row's
-   scale) is at least 2^3, or steps of 2^-9 where it is at least 2^6; half a
-   step each is 2^-16 of the largest at most, times codes up to 448:
+   steps of 2^-13 where the largest p_t s_t (s_t the value row's scale) is at
+   least 2^2: less than a step each, with a mean of 0 over the rows' dither, and
+   together less than half a step each, 2^-16 of the largest, times codes up to
+   448 (the shared prefix's fp16 weights stay within it):
        2^-9 A + n 2^-16 max_t(p_t s_t) 448;
  - bf16 outputs are rounded once: 2^-8 |o| (half a step), fp32: u32 |o|.
 """

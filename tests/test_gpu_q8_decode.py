@@ -10,6 +10,7 @@ import torch
 from grouped_query_attention_mqa_b200 import binding, q8
 from grouped_query_attention_mqa_b200.build import build
 
+from oracle import q8_oracle
 from q8_util import assert_within, attention, cache_parts, dev_cache, host_cache, round_to, rows
 
 pytestmark = pytest.mark.gpu
@@ -280,3 +281,49 @@ def test_refusals_raise():
         q8.append(cache, q[:1, :1], q[:1, :1], i32([0, 0]))
     empty = q8.new_cache(0, 8, 1, 128)
     assert q8.decode(q[:0], empty, i32([]), 1.0).shape == (0, 4, 128)
+
+
+@pytest.mark.parametrize("where", [0, 700, 19999])
+@pytest.mark.parametrize("h", [5, 24, 64])
+def test_tensor_cores_long_tail_behind_one_heavy_row(h, where):
+    """Row ``where`` outweighs each of 20,000 others by up to 2^17, so that the
+    others are below a weight's grid relative to it and yet a seventh of the
+    result: their weights' roundings, to steps of 2^-13 where the heavy row's P
+    is 2^2, must average out.  Weights of 2^-8 of the heavy one and more: 2^-8
+    of each at most.  Smaller ones: a rounding is off by less than a step, 2^-15
+    of the heavy weight, with a mean of 0 over the dither's 256 values; over n
+    rows 2^-15 n^1/2 / 2 is a standard deviation where all differ (half a step
+    each, |v| <= 2.5), and 5 of them are allowed."""
+    rng = np.random.default_rng(16)
+    n, gap = 20000, 17 * np.log(2)
+    K = np.zeros((1, n, 1, 128))
+    K[0, where, 0, 0] = 1.0
+    V = 1.5 + 0.5 * rng.standard_normal((1, n, 1, 128)).clip(-2, 2)
+    arrays = []
+    for x in (K, V):
+        c, e = q8_oracle.quantise(x)
+        arrays += [c, np.ascontiguousarray(np.moveaxis(e, 2, 1))]
+    q = np.zeros((1, h, 128))
+    q[0, :, 0] = np.linspace(0, 1, h)          # gaps of 0 to 17 octaves
+    q, q64 = round_to(q, "bf16")
+    o = q8.decode(q.cuda(), dev_cache(arrays), i32([n]), float(gap), num_ctas=1)
+    ref, tol = attention(q64, cache_parts(arrays, [n]), 1, gap, "bf16", two_terms=False)
+    heavy = np.exp(gap * q64[0, :, 0])
+    total = heavy + n - 1
+    grid = 5 * 2.0 ** -16 * 2.5 * np.sqrt(n) * heavy / total
+    M = q64[0, :, :1] * gap
+    tol = tol + np.abs(ref) * (2.0 ** -8 + 2 * 2.0 ** -10 / 224 * M) + grid[:, None]
+    assert_within(o, ref, tol)
+
+
+def test_tensor_cores_references_up_and_down():
+    """Heavy rows in some tiles and not in others, differently for each head."""
+    rng = np.random.default_rng(17)
+    n, h = 6000, 24
+    K = 0.02 * rng.standard_normal((1, n, 1, 128))
+    K[0, rng.integers(0, n, 40), 0, :] *= 40.0
+    arrays = []
+    for x in (K, rows(rng, (1, n, 1, 128), 3.0)):
+        c, e = q8_oracle.quantise(x)
+        arrays += [c, np.ascontiguousarray(np.moveaxis(e, 2, 1))]
+    run(rng, [n], h, 1, n, 128, 128, "bf16", "tcgen05", scale=1.0, ctas=1, arrays=arrays, q_spread=1.0)

@@ -8,6 +8,7 @@ import torch
 from grouped_query_attention_mqa_b200 import binding, q8
 from grouped_query_attention_mqa_b200.build import build
 
+from oracle import q8_oracle
 from q8_util import assert_within, attention, cache_parts, dev_cache, host_cache, round_to, rows
 
 pytestmark = pytest.mark.gpu
@@ -139,3 +140,67 @@ def test_steps_behind_a_shared_prompt():
             arrays[2 * i][:, t], arrays[2 * i + 1][:, :, t] = c, e
         ref, tol = attention(q64, parts_of(host_prefix, P, arrays, [t + 1] * b), g, 0.09, "bf16", two_terms=True)
         assert_within(step[1].out, ref, tol, f"step {t}")
+
+
+@pytest.mark.parametrize("spread", [4, 20])
+def test_values_of_very_different_size(spread):
+    """Value rows up to 2^spread apart within a tile, some of them zero, each
+    query on one row.  The unpacked values are off by at most 2^-25 units of
+    which their tile's largest row has scale 1: 2^-25 of the scale s."""
+    rng = np.random.default_rng(8)
+    n, b, h = 500, 40, 8
+    K = np.sign(rng.standard_normal((1, n, 1, 128)))
+    V = rng.standard_normal((1, n, 1, 128)) * np.exp2(rng.uniform(-spread / 2, spread / 2, (1, n, 1, 1)))
+    V[0, ::7] = 0
+    prefix = []
+    for x in (K, V):
+        c, e = q8_oracle.quantise(x)
+        prefix += [c, np.ascontiguousarray(np.moveaxis(e, 2, 1))]
+    at = rng.integers(0, n, (b, h))
+    q, q64 = round_to(K[0, at, 0], "bf16")
+    arrays = host_cache(rng, b, 2, 1, 128, lens=[0] * b)
+    o = q8.decode_shared(q.cuda(), dev_cache(prefix), i32([n]), dev_cache(arrays), i32([0] * b), 0.5)
+    ref, tol = attention(q64, parts_of(prefix, n, arrays, [0] * b), 1, 0.5, "bf16", two_terms=True)
+    # and weights to 2^-27 of the largest, relative to the tile's scale, times codes up to 448
+    s = q8_oracle.scale_of(prefix[3].astype(np.int64)).max()
+    assert_within(o, ref, tol + s * (2.0 ** -25 + 448 * 2.0 ** -27))
+
+
+def test_value_sizes_that_rise_along_the_prefix():
+    """Each tile's values 2^9 above the one before, and a run of zero rows first."""
+    rng = np.random.default_rng(9)
+    n = 640
+    V = rng.standard_normal((1, n, 2, 128)) * np.exp2(9.0 * (np.arange(n) // 64 - 5))[None, :, None, None]
+    for zeros in (0, 130):
+        V[0, :zeros] = 0
+        prefix = []
+        for x in (rng.standard_normal((1, n, 2, 128)), V):
+            c, e = q8_oracle.quantise(x)
+            prefix += [c, np.ascontiguousarray(np.moveaxis(e, 2, 1))]
+        run(rng, [3] * 9, 8, 2, n, n, 4, prefix=prefix, scale=0.3)
+        run(rng, [3] * 9, 8, 2, n, 100 + zeros // 5, 4, prefix=prefix, scale=0.3)
+
+
+def test_long_tail_behind_one_heavy_row():
+    """One prefix row outweighs each of 15,000 others by up to 2^17.  Weights are
+    fp16 numbers of which a reference starts at 2^2: half a step is 2^-25 at
+    most, 2^-27 of the heavy row's, and 2^-12 of a weight above 2^-14."""
+    rng = np.random.default_rng(10)
+    n, b, h, gap = 15000, 300, 64, 17 * np.log(2)
+    K = np.zeros((1, n, 1, 128))
+    K[0, 0, 0, 0] = 1.0
+    V = 1.5 + 0.5 * rng.standard_normal((1, n, 1, 128)).clip(-2, 2)
+    prefix = []
+    for x in (K, V):
+        c, e = q8_oracle.quantise(x)
+        prefix += [c, np.ascontiguousarray(np.moveaxis(e, 2, 1))]
+    q = np.zeros((1, h, 128))
+    q[0, :, 0] = np.linspace(0, 1, h)
+    q, q64 = round_to(q, "bf16")
+    arrays = host_cache(rng, 1, 2, 1, 128, lens=[0])
+    ref, tol = attention(q64, parts_of(prefix, n, arrays, [0]), 1, gap, "bf16", two_terms=False)
+    own = q8.new_cache(b, 2, 1, 128)
+    o = q8.decode_shared(q.cuda().expand(b, h, 128).contiguous(), dev_cache(prefix), i32([n]), own, i32([0] * b), float(gap))
+    M = q64[0, :, :1] * gap
+    tol = tol + np.abs(ref) * (2.0 ** -11 + 2 * 2.0 ** -10 / 224 * M) + n * 2.0 ** -27 * 2.5
+    assert_within(o, np.repeat(ref, b, 0), np.repeat(tol, b, 0))
