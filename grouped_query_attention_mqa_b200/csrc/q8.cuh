@@ -112,23 +112,35 @@ cudaError_t launch_q8_decode_tc(const TcArgs& a, const uint8_t* k, const uint8_t
 constexpr int kPrefixRows = 128, kPrefixKeys = 64;   // query rows of a block, keys of a tile
 constexpr int kPrefixMaxCtas = 512;
 __device__ __forceinline__ int prefix_tiles(int len) { return (len + kPrefixKeys - 1) / kPrefixKeys; }
-// How CTAs share the segments' tiles (`segs` of `nb` each, fewer than 2^31): the
-// first `more` CTAs take `each` + 1 of them, the others `each`.
+// How CTAs share the segments' tiles (`segs` of `nb` each).  A CTA that goes from
+// one segment to the next writes an output, converts queries and fills its
+// pipeline again, about kPrefixSeam tiles' time, so where CTAs have several
+// tiles a segment begins with as many units that are no tiles; a tile is a unit.
+// The first `more` CTAs take `each` + 1 units, the others `each`.  (128 GQA-8
+// sequences behind 16K rows, 54 tiles a CTA: 167 us with 0, 159 with 4, 155 with
+// 8, 160 with 12; 256 MQA ones behind 8K, 7 tiles: 45.5, 38.7 and 38.3 with 0, 4
+// and 8.)
+constexpr int kPrefixSeam = 8;
 struct PrefixShare {
-  int each, more;
-  __device__ __forceinline__ int start(int cta) const { return cta * each + min(cta, more); }
-  __device__ __forceinline__ int owner(int tile) const {
-    const int split = more * (each + 1);
-    return tile < split ? tile / (each + 1) : more + (tile - split) / each;
+  int nb, seam, ctas, each, more;
+  __device__ __forceinline__ PrefixShare(int segs, int nb_, int grid) : nb(nb_) {
+    seam = segs * nb >= 4 * grid ? kPrefixSeam : 0;
+    const int total = segs * (nb + seam);   // fewer than 2^31
+    ctas = min(total, grid);
+    each = total / ctas;
+    more = total - each * ctas;
+  }
+  __device__ __forceinline__ int start(int cta) const { return cta * each + min(cta, more); }   // its first unit
+  __device__ __forceinline__ int tile(int unit) const {   // tiles before a unit
+    if (seam == 0) return unit;
+    const int seg = unit / (nb + seam);
+    return seg * nb + max(unit - seg * (nb + seam) - seam, 0);
+  }
+  __device__ __forceinline__ int owner(int seg, int t) const {   // the CTA of a segment's tile
+    const int unit = seg * (nb + seam) + seam + t, split = more * (each + 1);
+    return unit < split ? unit / (each + 1) : more + (unit - split) / each;
   }
 };
-__device__ __forceinline__ PrefixShare prefix_share(int segs, int nb, int grid) {
-  const int total = segs * nb, ctas = min(total, grid);
-  PrefixShare s;
-  s.each = total / ctas;
-  s.more = total - s.each * ctas;
-  return s;
-}
 struct PrefixArgs {
   const __nv_bfloat16* q;
   const uint8_t* k;      // codes [m_p, g, d]

@@ -247,7 +247,8 @@ mqa_status_t mqa_q8_decode_shared(void* o, const void* q, const void* prefix_k, 
   if (int64_t(b) * g > (int64_t(1) << 29) || int64_t(b) * m_s * g > (int64_t(1) << 40) ||
       int64_t(m_p) * g > (int64_t(1) << 40) || int64_t(b) * h >= (int64_t(1) << 31) || !q8::q8_tc_fits(b, m_s) ||
       !q8::q8_tc_fits(1, m_p) || g > 65535 ||   // a grid dimension
-      ((int64_t(b) * (h / g) + q8::kPrefixRows - 1) / q8::kPrefixRows) * g * ((int64_t(m_p) + q8::kPrefixKeys - 1) / q8::kPrefixKeys) >=
+      ((int64_t(b) * (h / g) + q8::kPrefixRows - 1) / q8::kPrefixRows) * g *
+              ((int64_t(m_p) + q8::kPrefixKeys - 1) / q8::kPrefixKeys + q8::kPrefixSeam) >=
           (int64_t(1) << 31))
     return MQA_ERR_INVALID_ARG;   // past the kernels' index range
   const int hq = h / g;

@@ -40,9 +40,9 @@ __global__ void __launch_bounds__(kThreads) q8_merge_kernel(const TcArgs a, cons
     const unsigned row = unsigned(s) * unsigned(a.hq) + unsigned(i);
     const int seg = j * p.blocks + int(row / kPrefixRows);
     if (nb > 0) {
-      const PrefixShare share = prefix_share(a.g * p.blocks, nb, p.grid);
-      const int first = share.owner(seg * nb);
-      pre_n = share.owner(seg * nb + nb - 1) - first + 1;
+      const PrefixShare share(a.g * p.blocks, nb, p.grid);
+      const int first = share.owner(seg, 0);
+      pre_n = share.owner(seg, nb - 1) - first + 1;
       pre_at = (int64_t(first) + seg) * kPrefixRows + row % kPrefixRows;
     }
   }

@@ -23,28 +23,30 @@
 // weight.  fp16 spans 40 octaves: P starts at 2^2, a reference moves only when
 // some P would pass 2^15, and weights round to steps of 2^-24, 2^-26 of the
 // reference's: 2^18 rows that all lose half a step lose 2^-9 of it.  (Started at
-// 2^0: 186 us instead of 190 for 128 sequences behind a 16K prefix with GQA-8
-// and row scales that vary; at 2^4 195, at 2^8 228: the references move more
-// often.)
+// 2^4: 195 us instead of 190 for 128 sequences behind a 16K prefix with GQA-8
+// and row scales that vary, at 2^8 228: the references moved more often.)  The
+// maxima are taken before the exponentials; from the finished P, with a second
+// pass where one passes 2^15, that took 179 us instead of 155.
 // (The same product on the e4m3 codes as they are, with both operands in two
-// e4m3 terms and per-row scale tables: 158 us instead of 116 for that prefix,
-// the softmax threads' instructions, with a reference moving every third tile;
-// exponents of single rows brought to P where a tile's values are far apart: 10%
-// more for every call.)
+// e4m3 terms and per-row scale tables: 158 us for that prefix when this took
+// 116, with a reference moving every third tile; exponents of single rows
+// brought to P where a tile's values are far apart: 10% more for every call; a
+// quarter or half of the exponentials as a cubic on the FMA pipe: 4 to 10% more.)
 // Here query rows are the products' M, so that a row's softmax is one thread's
 // own: no barrier and no reduction across threads.
 //
 // Work: all (head, block) segments have the same number of tiles; the
-// persistent CTAs take equal contiguous runs of them, and every (CTA, segment)
-// leaves a normalised partial with its log-sum-exp for the merge.  Two CTAs per
+// persistent CTAs take equal contiguous runs of them (a segment's beginning
+// counted as some tiles more), and every (CTA, segment) leaves a normalised
+// partial with its log-sum-exp for the merge.  Two CTAs per
 // SM hide each other's chain of product, softmax and product.  Roles: warp 0 K
 // loads, warp 2 V loads, warp 1 S products, warp 3 P.V products (one lane
 // each), warps 4-7 queries, softmax and output, a row per thread.  Every wait is
 // bounded (one second) and reported with MQA_FLAG_PIPE_TIMEOUT.
 //
-// Bound: the softmax threads' instructions and latency (that prefix: 67 GFLOP
-// and 131 million exponentials in 116 us, 0.58 PFLOP/s; their floors are 41 and
-// 29 us).
+// Bound: the softmax threads' latency, tile after tile (that prefix: 67 GFLOP and
+// 131 million exponentials in about 85 us, 0.8 PFLOP/s; their floors are 41 and
+// 29 us), and at a CTA's ends the queries' conversion and the partial outputs.
 #include "q8_tc.cuh"
 
 namespace mqa {
@@ -58,7 +60,7 @@ constexpr int kRows = kPrefixRows, kKeys = kPrefixKeys;
 constexpr int kThreads = 256, kSoft = 128, kSoftWarp = 4;
 constexpr int kCtasPerSm = 2;
 constexpr int kRegsRoles = 72, kRegsSoft = 184;   // of the 128 per thread at launch
-constexpr float kTopP = 32768.f;                  // P stays below it: half of fp16's range
+constexpr float kTopLog = 15.f;                   // P stays below 2^15: half of fp16's range
 constexpr int kBias = 2;                          // the largest P after a reference is set is 2^kBias
 constexpr int kSK = 2, kSV = 2;                   // ring stages
 constexpr uint32_t kQHalf = kRows * 128, kHalf = kKeys * 128;   // 64 columns: 128-byte swizzled rows
@@ -344,66 +346,68 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
     }
     tc_fence_after();
     uint64_t y[kKeys / 2];     // y - M, in pairs
+    float top4[4];             // their largest, in four chains
+    auto largest = [&](int k) {
+      float y0, y1;
+      unpack2(y[k], y0, y1);
+      top4[k % 4] = fmaxf(fmaxf(top4[k % 4], y0), y1);
+    };
+    auto none = [&]() {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top4[k] = -INFINITY;
+    };
     {
       const uint64_t a2 = pack2(a_t, a_t), m2 = pack2(negm + shift, negm + shift);
+      none();
 #pragma unroll
       for (int ch = 0; ch < kKeys / 32; ++ch) {
         float s[32];
         tmem_ld32(t_lane + uint32_t(i & 1) * kKeys + ch * 32, s);
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) y[(ch * 32 + k) / 2] = fma2(pack2(s[k], s[k + 1]), a2, m2);
+        for (int k = 0; k < 32; k += 2) {
+          y[(ch * 32 + k) / 2] = fma2(pack2(s[k], s[k + 1]), a2, m2);
+          largest((ch * 32 + k) / 2);
+        }
       }
       tc_fence_before();
       mbar_arrive(bar(Cfg::kSEmpty + (i & 1)));   // the buffer may take S(i+2)
       if (valid < kKeys) {
+        none();
 #pragma unroll
         for (int k = 0; k < kKeys / 2; ++k) {
           float y0, y1;
           unpack2(y[k], y0, y1);
           y[k] = pack2(2 * k < valid ? y0 : -INFINITY, 2 * k + 1 < valid ? y1 : -INFINITY);
+          largest(k);
         }
       }
     }
-    // P in fp16; again with a moved reference if some row's passed 2^15
-    uint32_t p[kKeys / 2];
-    uint64_t sum2;
+    // A reference moves if some P of the warp's rows would pass 2^15.
     float alpha = 1.f;
-    bool move = first, moved = false;
-    for (;;) {
-      if (move) {
-        float top = -INFINITY;
+    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+    const bool move = first || __any_sync(0xffffffffu, top > kTopLog);
+    if (move) {
+      const float by = first ? top - float(kBias) : fmaxf(top - float(kBias), 0.f);
+      const uint64_t b2 = pack2(-by, -by);
 #pragma unroll
-        for (int k = 0; k < kKeys / 2; ++k) {
-          float y0, y1;
-          unpack2(y[k], y0, y1);
-          top = fmaxf(fmaxf(top, y0), y1);
-        }
-        const float by = first ? top - float(kBias) : fmaxf(top - float(kBias), 0.f);
-        const uint64_t b2 = pack2(-by, -by);
-#pragma unroll
-        for (int k = 0; k < kKeys / 2; ++k) y[k] = add2(y[k], b2);
-        negm -= by;
-        if (!first) {
-          alpha = ex2_approx(-by);
-          l *= alpha;
-          moved = true;
-        }
+      for (int k = 0; k < kKeys / 2; ++k) y[k] = add2(y[k], b2);
+      negm -= by;
+      if (!first) {
+        alpha = ex2_approx(-by);
+        l *= alpha;
       }
-      sum2 = 0;
-      __half2 big = __float2half2_rn(0.f);
+    }
+    // P in fp16
+    uint32_t p[kKeys / 2];
+    uint64_t sum2 = 0;
 #pragma unroll
-      for (int k = 0; k < kKeys / 2; ++k) {
-        float y0, y1;
-        unpack2(y[k], y0, y1);
-        const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
-        sum2 = add2(sum2, pack2(e0, e1));
-        const __half2 h = __floats2half2_rn(e0, e1);
-        big = __hmax2(big, h);
-        p[k] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      const float most = fmaxf(__low2float(big), __high2float(big));
-      if (move || !__any_sync(0xffffffffu, most > kTopP)) break;
-      move = true;
+    for (int k = 0; k < kKeys / 2; ++k) {
+      float y0, y1;
+      unpack2(y[k], y0, y1);
+      const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
+      sum2 = add2(sum2, pack2(e0, e1));
+      const __half2 h = __floats2half2_rn(e0, e1);
+      p[k] = *reinterpret_cast<const uint32_t*>(&h);
     }
     {
       float s0, s1;
@@ -416,7 +420,7 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
       break;
     }
     tc_fence_after();
-    if (moved) {               // collective for the warp; alpha = 1 in rows that keep theirs
+    if (move && !first) {      // collective for the warp; alpha = 1 in rows that keep theirs
 #pragma unroll
       for (int ch = 0; ch < kD / 32; ++ch) {
         float v[32];
@@ -530,11 +534,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   r.t0 = 0;
   r.n = 0;
   if (r.nb > 0) {
-    const int total = a.g * a.blocks * r.nb;
-    if (int(blockIdx.x) < total) {
-      const PrefixShare share = prefix_share(a.g * a.blocks, r.nb, a.grid);
-      r.t0 = share.start(blockIdx.x);
-      r.n = share.start(blockIdx.x + 1) - r.t0;
+    const PrefixShare share(a.g * a.blocks, r.nb, a.grid);
+    if (int(blockIdx.x) < share.ctas) {
+      r.t0 = share.tile(share.start(blockIdx.x));
+      r.n = share.tile(share.start(blockIdx.x + 1)) - r.t0;
     }
   }
   if (warp >= kSoftWarp) {

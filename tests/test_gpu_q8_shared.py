@@ -166,6 +166,11 @@ def test_values_of_very_different_size(spread):
     assert_within(o, ref, tol + s * (2.0 ** -25 + 448 * 2.0 ** -27))
 
 
+def test_many_blocks_with_long_runs():
+    """More segments than CTAs could take one each, several tiles a CTA."""
+    run(np.random.default_rng(11), [1, 0, 5] * 22, 64, 2, 2500, 2395, 5)
+
+
 def test_value_sizes_that_rise_along_the_prefix():
     """Each tile's values 2^9 above the one before, and a run of zero rows first."""
     rng = np.random.default_rng(9)
