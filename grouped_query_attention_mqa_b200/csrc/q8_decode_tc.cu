@@ -391,7 +391,7 @@ __device__ void producer(const TcArgs& a, const Run& run, const Roles& r, const 
 template <int HP>
 __device__ void s_issuer(const TcArgs& a, const Run& run, const Roles& r) {
   using C = Cfg<HP>;
-  constexpr uint32_t idesc = idesc_e4m3_f32(kRows, HP, 0, 0);
+  constexpr uint32_t idesc = idesc_code0_f32(kRows, HP, 0, 0);
   const uint64_t kdesc0 = smem_desc_sw128(r.sbase + C::kK, 16, 1024);   // K-major, rows of 128 bytes
   const uint64_t qdesc = smem_desc_sw128(r.sbase + C::kQ, 16, 1024);
   auto bar = [&](int id) { return r.sbase + C::kBar + 8u * uint32_t(id); };
@@ -431,7 +431,7 @@ __device__ void s_issuer(const TcArgs& a, const Run& run, const Roles& r) {
 template <int HP>
 __device__ void pv_issuer(const TcArgs& a, const Run& run, const Roles& r) {
   using C = Cfg<HP>;
-  constexpr uint32_t idesc = idesc_e4m3_f32(kD, C::kN, 1, 1);
+  constexpr uint32_t idesc = idesc_code0_f32(kD, C::kN, 1, 1);
   const uint64_t vdesc0 = smem_desc_sw128(r.sbase + C::kV, 16, 1024);   // MN-major: one 128-column atom, 8-row groups
   const uint64_t pdesc = smem_desc_sw128(r.sbase + C::kP, 16, 1024);
   auto bar = [&](int id) { return r.sbase + C::kBar + 8u * uint32_t(id); };

@@ -67,11 +67,6 @@ constexpr uint32_t kQHalf = kRows * 128, kHalf = kKeys * 128;   // 64 columns: 1
 constexpr uint32_t kTileBytes = 2 * kHalf;
 constexpr uint32_t kTmemCols = 256, kOCol = 2 * kKeys;   // S double buffer, then O
 
-// Instruction descriptor of tcgen05.mma kind::f16 with fp16 inputs (code 0).
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
-  return (1u << 4) | (uint32_t(a_mn_major) << 15) | (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
-}
-
 struct Cfg {
   static constexpr int kKFull = 0, kKEmpty = kSK, kVFull = 2 * kSK, kVEmpty = kVFull + kSV, kSFull = kVEmpty + kSV,
                        kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kOFull = kPFull + 1, kQFull = kOFull + 1,
@@ -221,7 +216,7 @@ __device__ void producer(const PrefixArgs& a, const Roles& r, const CUtensorMap*
 }
 
 __device__ void s_issuer(const Roles& r) {
-  constexpr uint32_t idesc = idesc_f16_f32(kRows, kKeys, 0, 0);
+  constexpr uint32_t idesc = idesc_code0_f32(kRows, kKeys, 0, 0);
   const uint64_t qdesc = smem_desc_sw128(r.sbase + Cfg::kQ, 16, 1024), kdesc0 = smem_desc_sw128(r.sbase + Cfg::kK, 16, 1024);
   auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };
   Walk w(r);
@@ -245,7 +240,7 @@ __device__ void s_issuer(const Roles& r) {
 }
 
 __device__ void pv_issuer(const Roles& r) {
-  constexpr uint32_t idesc = idesc_f16_f32(kRows, kD, 0, 1);
+  constexpr uint32_t idesc = idesc_code0_f32(kRows, kD, 0, 1);
   const uint64_t pdesc = smem_desc_sw128(r.sbase + Cfg::kP, 16, 1024);       // K-major: keys are K
   const uint64_t vdesc0 = smem_desc_sw128(r.sbase + Cfg::kV, kHalf, 1024);   // MN-major: columns are N
   auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };

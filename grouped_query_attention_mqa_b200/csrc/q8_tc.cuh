@@ -9,6 +9,56 @@
 #include "sm100.cuh"
 
 namespace mqa {
+namespace sm100 {
+
+// mbar_wait whose polls may sleep in hardware until the phase completes (up to
+// `kHintNs` each) instead of returning at once: several CTAs' waiting warps
+// then leave the issue slots to the ones that compute (78 -> 75 us where two
+// CTAs per SM take a prefix).
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  constexpr uint32_t kHintNs = 20000;
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kHintNs)
+        : "memory");
+    if (ok != 0) return true;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    else if (now - t0 > timeout_ns) return false;
+  }
+}
+
+// mma_bf16_ss with e4m3 inputs (K = 32 per instruction).
+__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of tcgen05.mma with fp32 sums and input formats of code
+// 0: e4m3 x e4m3 in kind::f8f6f4, fp16 x fp16 in kind::f16 (mma_bf16_ss); dense,
+// M x N, majors as in idesc_bf16_f32.
+__host__ __device__ constexpr uint32_t idesc_code0_f32(int M, int N, int a_mn_major, int b_mn_major) {
+  return (1u << 4)                       // D format: f32
+         | (uint32_t(a_mn_major) << 15)  // A major
+         | (uint32_t(b_mn_major) << 16)  // B major
+         | (uint32_t(N >> 3) << 17)      // N / 8
+         | (uint32_t(M >> 4) << 24);     // M / 16
+}
+
+}  // namespace sm100
+
 namespace q8 {
 
 constexpr int kD = 128;                          // head size
