@@ -327,3 +327,10 @@ def test_tensor_cores_references_up_and_down():
         c, e = q8_oracle.quantise(x)
         arrays += [c, np.ascontiguousarray(np.moveaxis(e, 2, 1))]
     run(rng, [n], h, 1, n, 128, 128, "bf16", "tcgen05", scale=1.0, ctas=1, arrays=arrays, q_spread=1.0)
+
+
+@pytest.mark.parametrize("h,g", [(200, 200), (700, 700), (303, 101)])
+def test_tensor_cores_many_kv_heads(h, g):
+    """More K/V heads than a grid has CTAs, or a number that does not divide it."""
+    run(np.random.default_rng(18), [150, 1, 0, 129], h, g, 150, 128, 128, "bf16", "tcgen05",
+        flag=binding.MQA_FLAG_LEN_CLAMPED)   # a decode reports an empty sequence

@@ -209,3 +209,46 @@ def test_long_tail_behind_one_heavy_row():
     M = q64[0, :, :1] * gap
     tol = tol + np.abs(ref) * (2.0 ** -11 + 2 * 2.0 ** -10 / 224 * M) + n * 2.0 ** -27 * 2.5
     assert_within(o, np.repeat(ref, b, 0), np.repeat(tol, b, 0))
+
+
+def test_captured_call_follows_the_lengths():
+    """One capture, replayed with other prefix and own lengths and queries in
+    the same buffers: from none of either to all."""
+    rng = np.random.default_rng(12)
+    b, h, g, m_p, m_s = 7, 24, 2, 900, 150
+    prefix, arrays = host_cache(rng, 1, m_p, g, 128), host_cache(rng, b, m_s, g, 128)
+    qd, p_len, lens_d = torch.zeros((b, h, 128), dtype=torch.bfloat16, device="cuda"), i32([0]), i32([0] * b)
+    plan = q8.SharedPlan(qd, dev_cache(prefix), p_len, dev_cache(arrays), lens_d, 0.1)
+    plan.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.run()
+    for P, lens in ((900, [150] * b), (0, [0] * b), (64, [0, 1, 2, 128, 129, 150, 0]), (1, [0] * b), (0, [3] * b), (899, [7] * b)):
+        q, q64 = round_to(rng.standard_normal((b, h, 128)), "bf16")
+        qd.copy_(q), p_len.fill_(P), lens_d.copy_(i32(lens))
+        graph.replay()
+        ref, tol = attention(q64, parts_of(prefix, P, arrays, lens), g, 0.1, "bf16", two_terms=True)
+        assert_within(plan.out, ref, tol, f"prefix {P}")
+
+
+def test_two_calls_at_once():
+    """Two plans, each with its workspace, on two streams without any order
+    between them: the same bits as one after the other."""
+    rng = np.random.default_rng(13)
+    plans = []
+    for h, g, m_p in ((32, 4, 3000), (8, 1, 5000)):
+        prefix, arrays = host_cache(rng, 1, m_p, g, 128), host_cache(rng, 20, 300, g, 128)
+        q, _ = round_to(rng.standard_normal((20, h, 128)), "bf16")
+        plans.append(q8.SharedPlan(q.cuda(), dev_cache(prefix), i32([m_p]), dev_cache(arrays),
+                                   i32(rng.integers(0, 301, 20).tolist()), 0.1))
+    want = [p.run().clone() for p in plans]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in plans]
+    for _ in range(20):
+        for p, s in zip(plans, streams):
+            with torch.cuda.stream(s):
+                p.run()
+    torch.cuda.synchronize()
+    for p, w in zip(plans, want):
+        assert torch.equal(p.out, w)
