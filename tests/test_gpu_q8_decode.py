@@ -334,3 +334,25 @@ def test_tensor_cores_many_kv_heads(h, g):
     """More K/V heads than a grid has CTAs, or a number that does not divide it."""
     run(np.random.default_rng(18), [150, 1, 0, 129], h, g, 150, 128, 128, "bf16", "tcgen05",
         flag=binding.MQA_FLAG_LEN_CLAMPED)   # a decode reports an empty sequence
+
+
+@pytest.mark.parametrize("path,dtype", [("tcgen05", torch.bfloat16), ("simt", torch.float32)])
+def test_offsets_past_32_bits(path, dtype):
+    """The last sequences of a cache of more than 2^32 codes against the same
+    sequences alone: the same bits."""
+    b, m, g = 65, 16384, 32
+    big = q8.new_cache(b, m, g, 128)
+    assert big.k.numel() > 2 ** 32
+    gen = torch.Generator("cuda").manual_seed(19)
+    lens = [0] * (b - 2) + [1500, 16384]
+    for t, top in ((big.k, 0x7f), (big.v, 0x7f)):   # no NaN
+        t.view(torch.uint8)[b - 2:] = torch.randint(0, top, (2, m, g, 128), generator=gen, device="cuda", dtype=torch.uint8)
+    for t in (big.k_exp, big.v_exp):
+        t[b - 2:] = torch.randint(115, 120, (2, g, m), generator=gen, device="cuda", dtype=torch.uint8)
+    small = q8.Cache(*(t[b - 2:].clone() for t in big))
+    q = torch.randn((b, 64, 128), generator=gen, device="cuda").to(dtype)
+    flags = i32([0])
+    o = q8.decode(q, big, i32(lens), 1e-3, path=path, status_flags=flags)
+    want = q8.decode(q[b - 2:].contiguous(), small, i32(lens[-2:]), 1e-3, path=path)
+    assert torch.equal(o[b - 2:], want) and not o[:b - 2].any() and want.float().abs().min() > 0
+    assert int(flags) == binding.MQA_FLAG_LEN_CLAMPED

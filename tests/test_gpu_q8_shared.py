@@ -252,3 +252,28 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for p, w in zip(plans, want):
         assert torch.equal(p.out, w)
+
+
+def test_prefix_past_32_bits():
+    """A prefix of more than 2^32 codes whose last rows outweigh the rest, against
+    the decode over the same rows."""
+    m_p, g = 530_000, 64
+    prefix = q8.new_cache(1, m_p, g, 128)
+    assert prefix.k.numel() > 2 ** 32
+    gen = torch.Generator("cuda").manual_seed(20)
+    for t in (prefix.k, prefix.v):
+        for r in range(0, m_p, 100_000):
+            n = min(100_000, m_p - r)
+            t.view(torch.uint8)[0, r:r + n] = torch.randint(0, 0x78, (n, g, 128), generator=gen, device="cuda", dtype=torch.uint8)
+    prefix.k_exp.fill_(118), prefix.v_exp.fill_(120)
+    q = torch.randn((1, g, 128), generator=gen, device="cuda").bfloat16()
+    heavy = (q[0].sign() * 256).to(torch.float8_e4m3fn)               # q . k is 128 mean|q| 256 / 512 and more
+    prefix.k[0, m_p - 70:] = heavy
+    own = q8.new_cache(1, 1, g, 128)
+    o = q8.decode_shared(q, prefix, i32([m_p]), own, i32([0]), 0.5)
+    want = q8.decode(q, prefix, i32([m_p]), 0.5)
+    V = prefix.v[0, m_p - 70:].float() / 128
+    near = V.mean(0)                                                   # the heavy rows weigh the same
+    # both: 2^-9 of a weight, 2^-8 of the output; the rest weighs nothing
+    tol = 2.0 ** -7 * V.abs().mean(0) + 2.0 ** -7 * near.abs()
+    assert ((o[0].float() - near).abs() <= tol).all() and ((want[0].float() - near).abs() <= tol).all()
