@@ -15,7 +15,7 @@
 //   S[r, t]  = x_r . k'_t              M = 128 query rows, N = 64 keys, K = 128
 //   y_{r,t}  = scale log2(e) w_r 2^A S[r, t] + B - B_0
 //   P[r, t]  = 2^(y - M_r)  in fp16    (11 bits: a weight is off by 2^-12 of itself at most)
-//   O[r, c] += sum_t P[r, t] v'_t[c]   M = 128, N = 128, K = 64 keys
+//   O[r, c] += sum_t P[r, t] v'_t[c]   M = 128, N = 128, K = 64 keys (P in tensor memory, where S was)
 //   l_r     += sum_t P[r, t] 2^(B_0 - B)   in fp32, before P is rounded
 //   o_r      = 2^B_0 O[r, :] / l_r
 // B_0 is the first tile's B: the value exponent enters with the logit, so that a
@@ -39,14 +39,21 @@
 // persistent CTAs take equal contiguous runs of them (a segment's beginning
 // counted as some tiles more), and every (CTA, segment) leaves a normalised
 // partial with its log-sum-exp for the merge.  Two CTAs per
-// SM hide each other's chain of product, softmax and product.  Roles: warp 0 K
+// SM hide each other's chain of product, softmax and product.  S has two buffers;
+// S(i+2) follows P.V(i), which reads P(i) from S(i)'s place.  Every barrier that
+// a role does not wait for tile by tile has one phase per buffer, so that none
+// is two phases ahead of what is waited for.  Roles: warp 0 K
 // loads, warp 2 V loads, warp 1 S products, warp 3 P.V products (one lane
 // each), warps 4-7 queries, softmax and output, a row per thread.  Every wait is
 // bounded (one second) and reported with MQA_FLAG_PIPE_TIMEOUT.
 //
-// Bound: the softmax threads' latency, tile after tile (that prefix: 67 GFLOP and
-// 131 million exponentials in about 85 us, 0.8 PFLOP/s; their floors are 41 and
-// 29 us), and at a CTA's ends the queries' conversion and the partial outputs.
+// Bound: shared memory (per 64-row tile 64 KB of operands read and 32 KB written,
+// about 770 cycles at 128 bytes each, of about 1,050 taken) and the softmax
+// threads' latency (that prefix: 67 GFLOP and 131 million exponentials in about
+// 80 us, 0.8 PFLOP/s; their floors are 41 and 29 us), and at a CTA's ends the
+// queries' conversion and the partial outputs.  With P in shared memory, 32 KB
+// more per tile, 150 us instead of 143 for that call if no row scales vary; a
+// second P buffer there changed nothing.
 #include "q8_tc.cuh"
 
 namespace mqa {
@@ -69,18 +76,18 @@ constexpr uint32_t kTmemCols = 256, kOCol = 2 * kKeys;   // S double buffer, the
 
 struct Cfg {
   static constexpr int kKFull = 0, kKEmpty = kSK, kVFull = 2 * kSK, kVEmpty = kVFull + kSV, kSFull = kVEmpty + kSV,
-                       kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kOFull = kPFull + 1, kQFull = kOFull + 1,
+                       kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kOFull = kPFull + 2, kQFull = kOFull + 2,
                        kDone = kQFull + 1, kNumBars = kDone + 1;
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = kQ + 2 * kQHalf;
   static constexpr uint32_t kV = kK + kSK * kTileBytes;
-  static constexpr uint32_t kP = kV + kSV * kTileBytes;             // a row's line: 64 fp16 weights
-  static constexpr uint32_t kBar = kP + kRows * 128;
+  static constexpr uint32_t kBox = kV + kSV * kTileBytes;           // outputs on their way: 32 columns of the rows
+  static constexpr uint32_t kBar = kBox + kRows * 128;
   static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
   static constexpr uint32_t kAbort = kTmemSlot + 4;
   static constexpr uint32_t kQw = kAbort + 4;                       // [128] query scales
   static constexpr uint32_t kAlloc = kQw + kRows * 4;
-  static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kP % 1024 == 0, "swizzle atoms need 1024-byte alignment");
+  static_assert(kK % 1024 == 0 && kV % 1024 == 0, "swizzle atoms need 1024-byte alignment");
   static_assert(kAlloc <= (233472 - kCtasPerSm * 1024) / kCtasPerSm, "shared memory budget");
   static_assert(128 * kRegsRoles + kSoft * kRegsSoft == kThreads * 128, "registers");
 };
@@ -241,21 +248,21 @@ __device__ void s_issuer(const Roles& r) {
 
 __device__ void pv_issuer(const Roles& r) {
   constexpr uint32_t idesc = idesc_code0_f32(kRows, kD, 0, 1);
-  const uint64_t pdesc = smem_desc_sw128(r.sbase + Cfg::kP, 16, 1024);       // K-major: keys are K
   const uint64_t vdesc0 = smem_desc_sw128(r.sbase + Cfg::kV, kHalf, 1024);   // MN-major: columns are N
   auto bar = [&](int id) { return r.sbase + Cfg::kBar + 8u * uint32_t(id); };
   Walk w(r);
   for (int i = 0; i < r.n; ++i) {
     w.next();
     const int st = i % kSV;
-    if (!wait_bar(r, bar(Cfg::kPFull), uint32_t(i) & 1)) break;
+    if (!wait_bar(r, bar(Cfg::kPFull + (i & 1)), uint32_t(i >> 1) & 1)) break;
     if (!wait_bar(r, bar(Cfg::kVFull + st), uint32_t(i / kSV) & 1)) break;
     tc_fence_after();
     const uint64_t va = vdesc0 + uint64_t((uint32_t(st) * kTileBytes) >> 4);
 #pragma unroll
     for (int kk = 0; kk < kKeys / 16; ++kk)
-      mma_bf16_ss(r.tmem + kOCol, pdesc + ((kk * 32) >> 4), va + ((kk * 2048) >> 4), idesc, !w.first || kk > 0);
-    mma_commit(bar(Cfg::kOFull));
+      mma_f16_ts(r.tmem + kOCol, r.tmem + uint32_t(i & 1) * kKeys + kk * 8, va + ((kk * 2048) >> 4), idesc, !w.first || kk > 0);
+    mma_commit(bar(Cfg::kOFull + (i & 1)));
+    mma_commit(bar(Cfg::kSEmpty + (i & 1)));   // the buffer may take S(i+2)
     mma_commit(bar(Cfg::kVEmpty + st));
   }
   mma_commit(bar(Cfg::kDone));
@@ -268,7 +275,6 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
   const int q4 = warp & 3, tid = threadIdx.x - 32 * kSoftWarp, row = 32 * q4 + lane;
   const uint32_t t_lane = r.tmem + (uint32_t(32 * q4) << 16);
   float* const qw = reinterpret_cast<float*>(r.smem + Cfg::kQw);
-  unsigned char* const line = r.smem + Cfg::kP + row * 128;
   const float c = a.scale * kLog2e;
   const int64_t rows_all = int64_t(a.b) * a.hq;
   Walk w(r);
@@ -364,8 +370,6 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
           largest((ch * 32 + k) / 2);
         }
       }
-      tc_fence_before();
-      mbar_arrive(bar(Cfg::kSEmpty + (i & 1)));   // the buffer may take S(i+2)
       if (valid < kKeys) {
         none();
 #pragma unroll
@@ -393,7 +397,7 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
       }
     }
     // P in fp16
-    uint32_t p[kKeys / 2];
+    float p[kKeys / 2];        // two fp16 each
     uint64_t sum2 = 0;
 #pragma unroll
     for (int k = 0; k < kKeys / 2; ++k) {
@@ -402,20 +406,19 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
       const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
       sum2 = add2(sum2, pack2(e0, e1));
       const __half2 h = __floats2half2_rn(e0, e1);
-      p[k] = *reinterpret_cast<const uint32_t*>(&h);
+      p[k] = *reinterpret_cast<const float*>(&h);
     }
     {
       float s0, s1;
       unpack2(sum2, s0, s1);
       l = fmaf(s0 + s1, __uint_as_float(uint32_t(127 - rise) << 23), l);
     }
-    // P.V(i-1) must be complete before O is rescaled and P overwritten.
-    if (i > 0 && !wait(Cfg::kOFull, uint32_t(i - 1) & 1)) {
-      failed = true;
-      break;
-    }
-    tc_fence_after();
     if (move && !first) {      // collective for the warp; alpha = 1 in rows that keep theirs
+      if (!wait(Cfg::kOFull + ((i - 1) & 1), uint32_t((i - 1) >> 1) & 1)) {   // O holds P.V(i-1)
+        failed = true;
+        break;
+      }
+      tc_fence_after();
 #pragma unroll
       for (int ch = 0; ch < kD / 32; ++ch) {
         float v[32];
@@ -424,28 +427,25 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
         for (int k = 0; k < 32; ++k) v[k] *= alpha;
         tmem_st<32>(t_lane + kOCol + ch * 32, v);
       }
-      tmem_wait_st();
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      *reinterpret_cast<uint4*>(line + ((j ^ (row & 7)) << 4)) = make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-    fence_proxy_async_smem();
+    tmem_st<32>(t_lane + uint32_t(i & 1) * kKeys, p);   // where S(i) was
+    tmem_wait_st();
     tc_fence_before();
-    mbar_arrive(bar(Cfg::kPFull));
+    mbar_arrive(bar(Cfg::kPFull + (i & 1)));
     if (last) {   // the segment's partial; then the next one's queries (its S products wait for them)
-      if (!wait(Cfg::kOFull, uint32_t(i) & 1)) {
+      if (!wait(Cfg::kOFull + (i & 1), uint32_t(i >> 1) & 1)) {
         failed = true;
         break;
       }
       tc_fence_after();
       const int64_t slot = int64_t(blockIdx.x) + seg;
       const float inv = scale_of(uint32_t(B0)) * rcp_approx(l);
-      // 32 columns at a time through the warp's own lines of P, so that whole
+      // 32 columns at a time through the warp's own part of the box, so that whole
       // 128-byte lines leave the SM (a row per lane, 32 bytes each, took four
       // times the requests: 5.5 us at the end of every CTA).
       const int rows_left = int(min(int64_t(kRows), rows_all - int64_t(seg % a.blocks) * kRows)) - 32 * q4;   // of this warp's 32
       const bool mine = lane < rows_left;
-      float4* const box = reinterpret_cast<float4*>(r.smem + Cfg::kP + q4 * 4096);   // [32 rows][8 pieces], swizzled
+      float4* const box = reinterpret_cast<float4*>(r.smem + Cfg::kBox + q4 * 4096);   // [32 rows][8 pieces], swizzled
       float* const dst = a.part_o + (slot * kRows + 32 * q4) * kD;
 #pragma unroll
       for (int ch = 0; ch < kD / 32; ++ch) {
@@ -501,10 +501,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(Cfg::kSFull + s), 1);
-      mbar_init(bar(Cfg::kSEmpty + s), kSoft);
+      mbar_init(bar(Cfg::kSEmpty + s), 1);
+      mbar_init(bar(Cfg::kPFull + s), kSoft);
+      mbar_init(bar(Cfg::kOFull + s), 1);
     }
-    mbar_init(bar(Cfg::kPFull), kSoft);
-    mbar_init(bar(Cfg::kOFull), 1);
     mbar_init(bar(Cfg::kQFull), kSoft);
     mbar_init(bar(Cfg::kDone), 2);   // one commit from each issuing thread
     *r.abort = 0;

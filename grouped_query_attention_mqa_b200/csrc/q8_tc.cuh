@@ -46,6 +46,18 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// mma_bf16_ss with the A operand in tensor memory: row m in lane m, two 16-bit
+// elements to a column (K-major), eight columns per instruction.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Instruction descriptor of tcgen05.mma with fp32 sums and input formats of code
 // 0: e4m3 x e4m3 in kind::f8f6f4, fp16 x fp16 in kind::f16 (mma_bf16_ss); dense,
 // M x N, majors as in idesc_bf16_f32.
