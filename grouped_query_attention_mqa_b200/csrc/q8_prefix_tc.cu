@@ -6,10 +6,11 @@
 // Two kernels.  The first unpacks the prefix to fp16, once for the whole batch:
 // tile by tile of 64 rows, each tile relative to its largest key and its largest
 // value exponent,
-//   k'_t = code_t 2^(a_t - A),   v'_t = code_t 2^(b_t - B)      (exact, a code has 4 bits; rows
-// 2^-9 and more below their tile's largest scale lose what is below 2^-25 of a
-// unit of which that row has up to 448), zeros past the prefix's end.  The
-// second is a product with a running softmax over query blocks: the rows of one K/V head are the pairs
+//   k'_t = code_t 2^(a_t - A),   v'_t = code_t 2^(b_t - B)
+// (a code is a multiple of 2^-9: exact down to 2^-15 of the tile's largest scale;
+// rows below that are rounded to steps of 2^-24 of it), zeros past the prefix's
+// end.  The second is a product with a running softmax over query blocks: the
+// rows of one K/V head are the pairs
 // (sequence, head of the group), in that order, and with x_r = q_r / w_r in
 // fp16 (maximum in (224, 448], bf16's 8 bits exact to 2^-17 of a unit)
 //   S[r, t]  = x_r . k'_t              M = 128 query rows, N = 64 keys, K = 128
@@ -141,14 +142,19 @@ __global__ void __launch_bounds__(kUnpackThreads) q8_unpack_kernel(const PrefixA
     const int t = (p / (kD / 16)) % kKeys, c = p % (kD / 16);
     const int d = int(e[x]) - (val ? B : A);   // 0 at most
     // rows of the smallest scale count as zeros where a tile's values have no other
-    const bool none = e[x] == 0 || d < -60 || (val && top_v == 0);
-    const __half2 f = __float2half2_rn(none ? 0.f : __uint_as_float(uint32_t(127 + d) << 23));
+    const bool none = e[x] == 0 || (val && top_v == 0);
+    // The factor 2^d in two, as fp16 ends at 2^-24: the first product is exact (a
+    // code is a multiple of 2^-9), the second rounds once.  From 2^-34 on nothing
+    // is left of any code.
+    const int d1 = max(d, -14), d2 = max(d - d1, -24);
+    const __half2 f1 = __float2half2_rn(none ? 0.f : __uint_as_float(uint32_t(127 + d1) << 23));
+    const __half2 f2 = __float2half2_rn(__uint_as_float(uint32_t(127 + d2) << 23));
     uint32_t h[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       uint32_t u;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(u) : "h"(uint16_t((&w[x].x)[k / 2] >> (16 * (k & 1)))));
-      const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&u), f);
+      const __half2 y = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&u), f1), f2);
       h[k] = *reinterpret_cast<const uint32_t*>(&y);
     }
     __half* const dst = (val ? a.v16 : a.k16) + out + t * kD + c * 16;

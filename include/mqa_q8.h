@@ -137,10 +137,11 @@ MQA_API mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, 
  *                     in fp16, unpacked anew by every call
  *
  * MQA_FLAG_LEN_CLAMPED reports lengths outside [0, m]; 0 is a length here.
- * The prefix's values count with 2^-25 of the largest value scale among the 64
- * rows from a multiple of 64 on, their weights with 2^-12 of themselves or 2^-27
- * of the largest p_t s_t, s_t that largest scale; such scales of one K/V head
- * are at most 2^126 apart.  The own rows are taken as by mqa_q8_decode.
+ * The prefix's keys and values are exact down to 2^-15 of the largest key or
+ * value scale among the 64 rows from a multiple of 64 on; rows of smaller scales
+ * are off by up to 2^-25 of it.  Their weights count with 2^-12 of themselves or
+ * 2^-27 of the largest p_t s_t, s_t that largest scale; such scales of one K/V
+ * head are at most 2^126 apart.  The own rows are taken as by mqa_q8_decode.
  * A sequence with no rows at all gets a zero row.  Built for bf16, d = 128
  * and h/g <= 64 (MQA_ERR_UNSUPPORTED otherwise).
  */
