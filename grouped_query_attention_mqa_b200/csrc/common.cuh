@@ -93,6 +93,13 @@ __host__ __device__ inline Workspace carve_workspace(void* base, int b, int g, i
 // collides, and slots < G + b*g.
 __device__ __forceinline__ int64_t partial_slot(int c, int64_t s) { return int64_t(c) + s; }
 
+// A segment's first and last CTA as seg_info names them.  A decode that gave up a wait
+// leaves some of them unwritten, and a workspace may hold anything: a merge
+// checks them before it uses them as indices, and writes NaN otherwise.
+__host__ __device__ inline bool parts_named(int2 info, int ctas) {
+  return info.x >= 0 && info.x <= info.y && info.y < ctas;
+}
+
 // ------------------------------------------------------------ work partition
 
 struct Sched {

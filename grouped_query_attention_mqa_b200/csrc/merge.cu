@@ -28,7 +28,7 @@ struct MergeArgs {
   const int32_t* lens;
   const int32_t* slens;
   Workspace ws;
-  int h, g, hq, d, m_max, q_beams, q_group_heads, m_s;
+  int h, g, hq, d, m_max, q_beams, q_group_heads, m_s, grid;
 };
 
 // One CTA per (segment, group of heads); each thread merges four consecutive
@@ -69,6 +69,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeArgs a,
   }
   const int2 info = a.ws.seg_info[s];
   if (info.x == info.y) return;
+  if (!parts_named(info, a.grid)) {   // the decode gave up, and its flag says so
+#pragma unroll
+    for (int k = 0; k < 4; ++k) O[k] = from_f32<T>(NAN);
+    return;
+  }
   // The loads of the first kParts partials go out together (one L2 round
   // trip), then they are combined; a segment split more ways takes the rest
   // one by one.
@@ -138,6 +143,7 @@ cudaError_t launch_merge(const DecodeArgs& da, mqa_dtype_t dtype, cudaStream_t s
   a.q_beams = da.q_beams;
   a.q_group_heads = da.q_group_heads;
   a.m_s = da.m_s;
+  a.grid = da.grid;
   const int b = da.b;
   const bool beams = da.sk != nullptr;
   const int heads_per_cta = kMergeThreads / (a.d / 4);

@@ -50,11 +50,17 @@ __global__ void __launch_bounds__(kThreads) q8_merge_kernel(const TcArgs a, cons
   asm volatile("griddepcontrol.launch_dependents;");
   if (!active) return;
   int own_first = 0, own_n = 0;
+  float empty = 0.f;                // what a row without parts holds
   if (has_own) {
     const int2 info = a.ws.seg_info[int64_t(s) * a.g + j];
-    if (info.y < 0) return;         // written whole
-    own_first = info.x;
-    own_n = info.y - info.x + 1;
+    if (info.y == -1) return;       // written whole
+    if (parts_named(info, a.groups)) {
+      own_first = info.x;
+      own_n = info.y - info.x + 1;
+    } else {                        // the decode gave up, and its flag says so
+      pre_n = 0;
+      empty = NAN;
+    }
   }
   const int n = own_n + pre_n;
   float m = -INFINITY, l = 0.f;
@@ -113,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) q8_merge_kernel(const TcArgs a, cons
       acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
     }
   }
-  const float inv = n > 0 ? 1.f / l : 0.f;   // no rows at all: zeros
+  const float inv = n > 0 ? 1.f / l : empty;   // no rows at all: zeros
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   uint2 out;
   out.x = *reinterpret_cast<const uint32_t*>(&lo);
