@@ -19,9 +19,9 @@
 //   O[r, c] += sum_t P[r, t] v'_t[c]   M = 128, N = 128, K = 64 keys (P in tensor memory, where S was)
 //   l_r     += sum_t P[r, t] 2^(B_0 - B)   in fp32, before P is rounded
 //   o_r      = 2^B_0 O[r, :] / l_r
-// B_0 is the first tile's B: the value exponent enters with the logit, so that a
-// reference M_r is the largest contribution to the output, not the largest
-// weight.  fp16 spans 40 octaves: P starts at 2^2, a reference moves only when
+// B_0 is the B of the first tile that has values (a tile of zeros has B = B_0 - 60
+// instead, whatever B_0 becomes): the value exponent enters with the logit, so that
+// a reference M_r is the largest contribution to the output, not the largest weight.  fp16 spans 40 octaves: P starts at 2^2, a reference moves only when
 // some P would pass 2^15, and weights round to steps of 2^-24, 2^-26 of the
 // reference's: 2^18 rows that all lose half a step lose 2^-9 of it.  (Started at
 // 2^4: 195 us instead of 190 for 128 sequences behind a 16K prefix with GQA-8
@@ -327,7 +327,7 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
   const int2* tile_exps = a.tile_exps + w.seg / a.blocks * a.tiles;
   int2 exps = tile_exps[w.k];   // the next tile's A and B
   float negm = 0.f, l = 0.f, rw = 0.f;   // minus the row's reference, its sum, its query scale
-  int B0 = 119;
+  int B0 = 0;                            // 0: no value yet
   bool failed = !query_scale(0, rw);
   for (int i = 0; i < r.n && !failed; ++i) {
     const bool first = w.first;
@@ -341,11 +341,12 @@ __device__ void softmax(const PrefixArgs& a, const Roles& r, int warp, int lane)
     }
     const bool last = i + 1 == r.n || w.first;
     if (first) {
-      B0 = e.y > 0 ? e.y : 119;   // no value yet: any exponent does
       negm = 0.f;
       l = 0.f;
     }
-    const int rise = e.y > 0 ? min(max(e.y - B0, -126), 126) : 0;   // B - B_0
+    if (first || B0 == 0) B0 = e.y;   // O is 0 so far, and l does not depend on B_0
+    // B - B_0; a tile of zeros counts for little in the references, not for nothing
+    const int rise = e.y > 0 ? min(max(e.y - B0, -126), 126) : -kSpan;
     const float a_t = rw * scale_of(uint32_t(e.x)), shift = float(rise);
     if (!wait(Cfg::kSFull + (i & 1), uint32_t(i >> 1) & 1)) {
       failed = true;

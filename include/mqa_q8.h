@@ -141,7 +141,8 @@ MQA_API mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, 
  * value scale among the 64 rows from a multiple of 64 on; rows of smaller scales
  * are off by up to 2^-25 of it.  Their weights count with 2^-12 of themselves or
  * 2^-27 of the largest p_t s_t, s_t that largest scale; such scales of one K/V
- * head are at most 2^126 apart.  The own rows are taken as by mqa_q8_decode.
+ * head are at most 2^126 apart, and 64 rows of zeros count as 2^-60 of the first
+ * that is none of zeros.  The own rows are taken as by mqa_q8_decode.
  * A sequence with no rows at all gets a zero row.  Built for bf16, d = 128
  * and h/g <= 64 (MQA_ERR_UNSUPPORTED otherwise).
  */

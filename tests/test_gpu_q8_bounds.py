@@ -31,7 +31,7 @@ import torch
 from grouped_query_attention_mqa_b200 import q8
 from grouped_query_attention_mqa_b200.build import build
 from oracle import q8_oracle
-from q8_util import U32, assert_within, dev_cache, round_to
+from q8_util import U32, assert_within, dev_cache, host_cache, round_to
 
 pytestmark = pytest.mark.gpu
 
@@ -99,6 +99,20 @@ def within(o, q64, arrays, n, g, scale, shared):
     assert_within(o, ref, tol, "shared" if shared else "decode")
 
 
+def behind_prefix(q, arrays, n, g, scale):
+    """The rows as a prefix behind which every sequence has no rows of its own: a
+    few sequences and, so that a CTA takes many tiles, very many with the same
+    queries."""
+    q, q64 = round_to(q, "bf16")
+    b, h = q.shape[:2]
+    prefix = dev_cache(arrays)
+    for copies in (1, 1 + (1 << 16) // (b * h)):
+        o = q8.decode_shared(q.cuda().repeat(copies, 1, 1), prefix, i32([n]), q8.new_cache(b * copies, 1, g, 128),
+                             i32([0] * (b * copies)), scale).view(copies, b, h, 128)
+        for c in range(0, copies, 1 + copies // 7):
+            within(o[c], q64, arrays, n, g, scale, True)
+
+
 # ------------------------------------------------------------------ scales far apart within a tile
 
 
@@ -140,3 +154,44 @@ def test_prefix_keys_far_below_their_tiles(apart):
     prefix = quantised(K, rng.standard_normal((1, n, 1, 128)))
     o = q8.decode_shared(q.cuda(), dev_cache(prefix), i32([n]), q8.new_cache(b, 1, 1, 128), i32([0] * b), 0.2)
     within(o, q64, prefix, n, 1, 0.2, True)
+
+
+# ------------------------------------------------------------------ rows of zeros first
+
+
+def values_after_zeros(rng, zeros, e, n, g):
+    """A cache of n rows, the first of them without a value, the others of scale 2^(e-127)."""
+    arrays = host_cache(rng, 1, n, g, 128, spread=0.3)
+    arrays[2] = q8_oracle.quantise(rng.choice([-1.0, 1.0], (1, n, g, 128)) * rng.uniform(8, 15, (1, n, g, 128)))[0]
+    if e == 250:
+        arrays[2] -= 5 << 3             # codes of 128 to 448, 2^-5 of them: below 2^127
+    arrays[2][:, :zeros], arrays[3][...] = 0, e
+    arrays[3][:, :, :zeros] = 1         # as the append leaves zeros
+    return arrays
+
+
+def heavy_zeros(rng, gap, n, heavy):
+    """A cache of n rows and queries; the first rows have no value and outweigh the others by 2^gap."""
+    K = 0.05 * rng.standard_normal((1, n, 1, 128))
+    K[0, :heavy, 0, 0] += gap * np.log(2)
+    V = rng.standard_normal((1, n, 1, 128))
+    V[0, :heavy] = 0
+    q = 0.05 * rng.standard_normal((3, 8, 128))
+    q[..., 0] = 1
+    return quantised(K, V), q
+
+
+@pytest.mark.parametrize("e", [40, 60, 87, 107, 127, 200, 250])
+@pytest.mark.parametrize("zeros", [64, 130])
+def test_prefix_values_after_tiles_of_zeros(zeros, e):
+    """Whole tiles without a value, then values of one scale, whatever it is."""
+    rng = np.random.default_rng(zeros + e)
+    arrays = values_after_zeros(rng, zeros, e, 400, 2)
+    behind_prefix(rng.standard_normal((5, 16, 128)), arrays, 400, 2, 0.09)
+
+
+@pytest.mark.parametrize("gap", [20, 40])
+def test_prefix_values_behind_heavy_tiles_of_zeros(gap):
+    rng = np.random.default_rng(gap)
+    arrays, q = heavy_zeros(rng, gap, 300, 128)
+    behind_prefix(q, arrays, 300, 1, 1.0)
