@@ -20,8 +20,8 @@
 //   P_{t,i}    = p_{t,i} b_t 2^(2-E)
 //   O^T[c, n] += sum_t v_t[c] P[t, n]   M = 128 columns of V, N = 2 heads, K = 128 rows
 //   o_i        = 2^(E-2) (O[c, i] + O[c, i'] / 16) / l_i
-// E is the largest value-row exponent seen (of rows that are not all zero) and
-// m_i is set so that the largest P is 2^2: the e4m3 grid (at least 2^-13 in the
+// E is the largest value-row exponent seen (of rows that are not all zero; 1, the
+// smallest, before any) and m_i is set so that the largest P is 2^2: the e4m3 grid (at least 2^-13 in the
 // second term) then lies relative to what a row contributes to the output, not
 // to its weight alone, and a heavy row with small values (an attention sink)
 // leaves the other rows their precision.  A reference is moved only when some P
@@ -66,6 +66,7 @@ constexpr int kCtasPerSm = 2;
 constexpr uint32_t kTileBytes = kRows * kD;     // 128 rows of codes, 128-byte swizzled
 constexpr int kSegUnits = 7;                    // cost of entering a segment, in quarter tiles (measured: 2.7 us, a tile 1.6)
 constexpr int kBias = 2;                        // the largest P after a reference is set is 2^kBias
+constexpr float kFall = 90.f;                    // octaves that a reference comes down at a time: the sums stay finite
 constexpr int kLensCache = 256;
 constexpr uint32_t kMaxDynSmem = (233472 - kCtasPerSm * 1024) / kCtasPerSm;
 
@@ -665,7 +666,7 @@ __device__ void softmax_epilogue(const TcArgs& a, const Run& run, const Roles& r
       const int em = max(max(e4[0], e4[1]), max(e4[2], e4[3]));
       const int E_old = E;
       if (first) any = false;
-      E = any ? max(E, em) : em > 0 ? em : 119;   // no value yet: a middling 2^-8
+      E = any ? max(E, em) : max(em, 1);   // no value yet: the smallest, so that any value exceeds it
       any = any || em > 0;
       const float off = float(max(er - E, -kSpan));
       float mine = 0.f;      // lane k's: column k's maximum
@@ -698,7 +699,7 @@ __device__ void softmax_epilogue(const TcArgs& a, const Run& run, const Roles& r
         float by = fmaxf(fmaxf(red[col], red[HP + col]), fmaxf(red[2 * HP + col], red[3 * HP + col]));
         if (!first) {
           const float shift = float(E_old - E);   // the old reference relative to E
-          by = fmaxf(by, shift);
+          by = fmaxf(by, fmaxf(shift, -kFall));
           moves = by != shift;
           alpha_l[lane] = ex2_approx(-by);
           alpha_o[lane] = ex2_approx(shift - by);

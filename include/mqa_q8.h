@@ -103,7 +103,8 @@ MQA_API mqa_status_t mqa_q8_read(void* k_out, void* v_out, const void* k_codes, 
  * tensor-core path a row's weight is rounded to 2^-9 of itself, or to steps of
  * 2^-15 of the largest p_t s_t (weight times value scale) where that is more,
  * up or down as often as its size says; a query's elements to 2^-17 of its
- * largest.
+ * largest.  There the value scales of one K/V head's rows, rows of zeros aside,
+ * are at most 2^100 apart.
  * Paths: the tensor-core path takes bf16 with d_k = d_v = 128 and h/g <= 64,
  * and is then the automatic choice; the CUDA-core path takes both types with
  * d_k, d_v in {32, 64, 128} and h/g * d_k, h/g * d_v <= 4096.

@@ -113,6 +113,16 @@ def behind_prefix(q, arrays, n, g, scale):
             within(o[c], q64, arrays, n, g, scale, True)
 
 
+def over_own_rows(q, arrays, n, g, scale):
+    """The rows as a sequence's own cache, its tiles split between CTAs and not."""
+    q, q64 = round_to(q, "bf16")
+    cache = dev_cache(arrays)
+    for ctas in (0, 1):
+        for s in range(min(q.shape[0], 2)):
+            o = q8.decode(q[s:s + 1].cuda(), cache, i32([n]), scale, path="tcgen05", num_ctas=ctas)
+            within(o, q64[s:s + 1], arrays, n, g, scale, False)
+
+
 # ------------------------------------------------------------------ scales far apart within a tile
 
 
@@ -195,3 +205,19 @@ def test_prefix_values_behind_heavy_tiles_of_zeros(gap):
     rng = np.random.default_rng(gap)
     arrays, q = heavy_zeros(rng, gap, 300, 128)
     behind_prefix(q, arrays, 300, 1, 1.0)
+
+
+@pytest.mark.parametrize("e", [5, 20, 40, 60, 87, 127, 200, 250])
+@pytest.mark.parametrize("h", [16, 128])       # all heads in a thread, or half of them
+@pytest.mark.parametrize("zeros", [128, 260])
+def test_own_values_after_tiles_of_zeros(zeros, h, e):
+    rng = np.random.default_rng(zeros + e + h)
+    arrays = values_after_zeros(rng, zeros, e, 700, 2)
+    over_own_rows(rng.standard_normal((2, h, 128)), arrays, 700, 2, 0.09)
+
+
+@pytest.mark.parametrize("gap", [20, 40, 80])
+def test_own_values_behind_heavy_tiles_of_zeros(gap):
+    rng = np.random.default_rng(gap)
+    arrays, q = heavy_zeros(rng, gap, 600, 256)
+    over_own_rows(q, arrays, 600, 1, 1.0)
