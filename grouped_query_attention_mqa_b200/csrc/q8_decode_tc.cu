@@ -9,9 +9,10 @@
 // With w the power of two that puts a bf16 query's maximum in (224, 448], q1 +
 // q2 is exact for elements above 2^-10 of it and off by at most 2^-10 units
 // (2^-17 of the maximum) below; both terms' products add up in one
-// accumulator.  A weight is off by at most 2^-9 of itself (a bf16 weight:
-// 2^-8); its terms are columns side by side whose results are joined at the
-// end, which gives the second term 4 more octaves before it underflows.
+// accumulator.  A weight is off by at most 2^-9 of itself by its terms and 2^-11
+// by the fp16 number that they are taken from (a bf16 weight: 2^-8); its terms are
+// columns side by side whose results are joined at the end, which gives the second
+// term 4 more octaves before it underflows.
 //
 // With k_t, v_t the codes and a_t, b_t the row scales:
 //   S^T[t, i]  = k_t . (q1_i + q2_i)    M = 128 rows, N = heads, K = 2 x 128

@@ -15,7 +15,7 @@
 // fp16 (maximum in (224, 448], bf16's 8 bits exact to 2^-17 of a unit)
 //   S[r, t]  = x_r . k'_t              M = 128 query rows, N = 64 keys, K = 128
 //   y_{r,t}  = scale log2(e) w_r 2^A S[r, t] + B - B_0
-//   P[r, t]  = 2^(y - M_r)  in fp16    (11 bits: a weight is off by 2^-12 of itself at most)
+//   P[r, t]  = 2^(y - M_r)  in fp16    (11 bits: a weight is off by 2^-11 of itself at most)
 //   O[r, c] += sum_t P[r, t] v'_t[c]   M = 128, N = 128, K = 64 keys (P in tensor memory, where S was)
 //   l_r     += sum_t P[r, t] 2^(B_0 - B)   in fp32, before P is rounded
 //   o_r      = 2^B_0 O[r, :] / l_r

@@ -100,10 +100,10 @@ MQA_API mqa_status_t mqa_q8_read(void* k_out, void* v_out, const void* k_codes, 
  *
  * Rows at or past lens[b], and rows before the window, never count, whatever
  * codes and exponents they hold.  Statistics and sums are fp32.  On the
- * tensor-core path a row's weight is rounded to 2^-9 of itself, or to steps of
- * 2^-15 of the largest p_t s_t (weight times value scale) where that is more,
- * up or down as often as its size says; a query's elements to 2^-17 of its
- * largest.  There the value scales of one K/V head's rows, rows of zeros aside,
+ * tensor-core path a row's weight is off by at most 2^-9 + 2^-11 of itself and
+ * less than a step of 2^-15 of the largest p_t s_t (weight times value scale),
+ * up or down as often as its size says; a query's elements by at most 2^-17 of
+ * its largest.  There the value scales of one K/V head's rows, rows of zeros aside,
  * are at most 2^100 apart.
  * Paths: the tensor-core path takes bf16 with d_k = d_v = 128 and h/g <= 64,
  * and is then the automatic choice; the CUDA-core path takes both types with
@@ -140,10 +140,10 @@ MQA_API mqa_status_t mqa_q8_decode(void* o, const void* q, const void* k_codes, 
  * MQA_FLAG_LEN_CLAMPED reports lengths outside [0, m]; 0 is a length here.
  * The prefix's keys and values are exact down to 2^-15 of the largest key or
  * value scale among the 64 rows from a multiple of 64 on; rows of smaller scales
- * are off by up to 2^-25 of it.  Their weights count with 2^-12 of themselves or
- * 2^-27 of the largest p_t s_t, s_t that largest scale; such scales of one K/V
- * head are at most 2^126 apart, and 64 rows of zeros count as 2^-60 of the first
- * that is none of zeros.  The own rows are taken as by mqa_q8_decode.
+ * are off by up to 2^-25 of it.  Their weights are off by at most 2^-11 of
+ * themselves or 2^-27 of the largest p_t s_t, s_t that largest scale; such scales
+ * of one K/V head are at most 2^126 apart, and 64 rows of zeros count as 2^-60 of
+ * the first that is none of zeros.  The own rows are taken as by mqa_q8_decode.
  * A sequence with no rows at all gets a zero row.  Built for bf16, d = 128
  * and h/g <= 64 (MQA_ERR_UNSUPPORTED otherwise).
  */
