@@ -31,7 +31,7 @@ import torch
 from grouped_query_attention_mqa_b200 import q8
 from grouped_query_attention_mqa_b200.build import build
 from oracle import q8_oracle
-from q8_util import U32, assert_within, dev_cache, host_cache, round_to
+from q8_util import U32, assert_within, dev_cache, host_cache, round_to, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -221,3 +221,51 @@ def test_own_values_behind_heavy_tiles_of_zeros(gap):
     rng = np.random.default_rng(gap)
     arrays, q = heavy_zeros(rng, gap, 600, 256)
     over_own_rows(q, arrays, 600, 1, 1.0)
+
+
+# ------------------------------------------------------------------ many rows, sharp softmaxes, scales of every size
+
+
+@pytest.mark.parametrize("n,g,h,scale,spread", [
+    (1500, 2, 16, 0.09, 1.0), (1500, 1, 32, 0.09, 4.0), (6000, 1, 24, 0.3, 3.0), (2500, 1, 64, 1.0, 1.0),
+    (3000, 2, 8, 0.0, 6.0), (700, 1, 8, 0.2, 0.2)])
+def test_random_rows(n, g, h, scale, spread):
+    rng = np.random.default_rng(n + h)
+    arrays, q = host_cache(rng, 1, n, g, 128, spread=spread), rng.standard_normal((6, h, 128))
+    behind_prefix(q, arrays, n, g, scale)
+    over_own_rows(q, arrays, n, g, scale)
+
+
+@pytest.mark.parametrize("gap", [4, 12, 20])
+def test_some_rows_dominate(gap):
+    """One row in 97 outweighs the others by about 2^gap, its values as large as
+    theirs or 2^-7 of them."""
+    rng = np.random.default_rng(30 + gap)
+    n, h = 3000, 32
+    K = 0.3 * rng.standard_normal((1, n, 1, 128))
+    K[0, ::97, 0, 0] += gap * np.log(2)
+    V = rows(rng, (1, n, 1, 128))
+    q = 0.3 * rng.standard_normal((4, h, 128))
+    q[..., 0] = 1
+    for small in (False, True):
+        if small:
+            V[0, ::97] *= 2.0 ** -7
+        behind_prefix(q, quantised(K, V), n, 1, 1.0)
+        over_own_rows(q, quantised(K, V), n, 1, 1.0)
+
+
+# ------------------------------------------------------------------ the same bits again
+
+
+@pytest.mark.parametrize("op", ["decode", "shared"])
+def test_a_call_repeats_itself(op):
+    rng = np.random.default_rng(40)
+    n, b, g, h = 2000, 12, 2, 32
+    prefix, cache = (dev_cache(host_cache(rng, x, y, g, 128)) for x, y in ((1, 1000), (b, n)))
+    lens = i32(rng.integers(1, n + 1, b).tolist())
+    q = round_to(rng.standard_normal((b, h, 128)), "bf16")[0].cuda()
+    plan = q8.DecodePlan(q, cache, lens, 0.1) if op == "decode" else q8.SharedPlan(q, prefix, i32([999]), cache, lens, 0.1)
+    first = plan.run().clone()
+    for _ in range(50):
+        plan.out.fill_(float("nan"))
+        assert torch.equal(plan.run(), first)
