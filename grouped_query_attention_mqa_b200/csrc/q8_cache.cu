@@ -67,9 +67,10 @@ __device__ __forceinline__ void locate_rows(Place* where, int r0, int rows, cons
     while (found != 0) {   // the warp's lanes share each such sequence's rows
       const int x = __ffs(found) - 1;
       found &= found - 1;
-      const int xlo = __shfl_sync(0xffffffffu, lo, x), xhi = __shfl_sync(0xffffffffu, hi, x);
+      // from the block's first row on: r0 + 31 may be past an int
+      const int xlo = __shfl_sync(0xffffffffu, lo, x) - r0, xhi = __shfl_sync(0xffffffffu, hi, x) - r0;
       const int64_t xp = __shfl_sync(0xffffffffu, (long long)p, x);
-      for (int r = xlo + lane; r < xhi; r += 32) where[r - r0] = place(s0 + x, xp + (r - xlo));
+      for (int r = xlo + lane; r < xhi; r += 32) where[r] = place(s0 + x, xp + (r - xlo));
     }
   }
   __syncthreads();
@@ -271,7 +272,7 @@ cudaError_t launch(CacheArgs& a, int d_k, int d_v, mqa_dtype_t dtype, cudaStream
   // exact for the block's rows x heads, at most 8 kThreads pieces when it has several rows
   a.g_inverse = a.rows == 1 ? 0u : unsigned((uint64_t(1) << 32) / unsigned(a.g)) + 1u;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((a.total + a.rows - 1) / a.rows), 2);
+  cfg.gridDim = dim3(unsigned((int64_t(a.total) + a.rows - 1) / a.rows), 2);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

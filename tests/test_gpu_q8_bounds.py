@@ -269,3 +269,17 @@ def test_a_call_repeats_itself(op):
     for _ in range(50):
         plan.out.fill_(float("nan"))
         assert torch.equal(plan.run(), first)
+
+
+def test_the_largest_append():
+    """As many packed rows as an int counts, all but one of no sequence."""
+    total = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 70 << 30:
+        pytest.skip("needs 70 GB free")
+    k = torch.empty((total, 1, 16), dtype=torch.bfloat16, device="cuda")
+    k[total - 1] = torch.arange(16, device="cuda") - 7.5
+    cache = q8.new_cache(1, 4, 1, 16)
+    q8.append(cache, k, k, i32([2]), cu_new=i32([total - 1, total]))
+    x, _ = q8.read(cache, i32([0, 4]), 4, dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert torch.equal(x[2, 0].cpu(), torch.arange(16) - 7.5) and not x[[0, 1, 3]].any()
