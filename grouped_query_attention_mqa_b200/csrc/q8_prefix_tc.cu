@@ -559,6 +559,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(r.tmem, kTmemCols);
+  // Without tiles nothing here has waited yet: what follows takes this grid's end
+  // for the unpacking's too.
+  if (r.n == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Unpacked rows [g, rows, 128] fp16 as (128, rows, g); a box is 64 columns of
