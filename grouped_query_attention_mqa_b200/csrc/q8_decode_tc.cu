@@ -18,15 +18,18 @@
 //   S^T[t, i]  = k_t . (q1_i + q2_i)    M = 128 rows, N = heads, K = 2 x 128
 //   s_{t,i}    = scale log2(e) w_i a_t S[t, i]
 //   p_{t,i}    = 2^(s_{t,i} - m_i),     l_i = sum_t p_{t,i}            (fp32)
-//   P_{t,i}    = p_{t,i} b_t 2^(2-E)
+//   P_{t,i}    = p_{t,i} b_t 2^(4-E)
 //   O^T[c, n] += sum_t v_t[c] P[t, n]   M = 128 columns of V, N = 2 heads, K = 128 rows
-//   o_i        = 2^(E-2) (O[c, i] + O[c, i'] / 16) / l_i
+//   o_i        = 2^(E-4) (O[c, i] + O[c, i'] / 16) / l_i
 // E is the largest value-row exponent seen (of rows that are not all zero; 1, the
-// smallest, before any) and m_i is set so that the largest P is 2^2: the e4m3 grid (at least 2^-13 in the
-// second term) then lies relative to what a row contributes to the output, not
-// to its weight alone, and a heavy row with small values (an attention sink)
-// leaves the other rows their precision.  A reference is moved only when some P
-// would pass 448.  Behind a heavy row a long tail's weights can all be below
+// smallest, before any) and m_i is set so that the largest P is 2^4: the e4m3 grid
+// (at least 2^-13 in the second term) then lies relative to what a row contributes
+// to the output, not to its weight alone, and a heavy row with small values (an
+// attention sink) leaves the other rows their precision.  A reference is moved only
+// when some P would pass 448.  (Relative errors over 32K rows, queries three times
+// as large as normal ones: 0.00159, of which 0.00158 is the output's rounding; with
+// 2^2 0.00165, 0 to 1% faster; with 2^6 0.00159, 0.5 to 1.7% slower; a bf16 decode of
+// the same values 0.0020.)  Behind a heavy row a long tail's weights can all be below
 // that grid: they are dithered before they are rounded, so that their sum stays
 // (lowering a reference with a tile's maxima instead cost 24% on 32K-row GQA-8
 // caches whose row scales vary: it goes up and down all the time).
@@ -34,7 +37,7 @@
 // Work: two persistent CTAs per SM (a tile's chain of product, softmax and
 // product is latency; two chains hide each other's).  CTA c serves K/V head c %
 // g over a contiguous run of all sequences' 128-row tiles, balanced in quarter
-// tiles with a segment's entry weighed as a whole tile.  The g CTAs of a group
+// tiles with a segment's entry weighed as kSegUnits of them.  The g CTAs of a group
 // walk the same rows in step: a cache row's g heads are neighbours in memory,
 // 128 bytes each, and reading them together is what DRAM pages want (32 GQA-8
 // caches of 8K to 32K rows, 1.44 GB: 287 us head by head, 237 in step).
@@ -66,7 +69,7 @@ constexpr int kKWarp = 0, kSWarp = 1, kVWarp = 2, kSoftWarp = 4;   // warp 3: P.
 constexpr int kCtasPerSm = 2;
 constexpr uint32_t kTileBytes = kRows * kD;     // 128 rows of codes, 128-byte swizzled
 constexpr int kSegUnits = 7;                    // cost of entering a segment, in quarter tiles (measured: 2.7 us, a tile 1.6)
-constexpr int kBias = 2;                        // the largest P after a reference is set is 2^kBias
+constexpr int kBias = 4;                        // the largest P after a reference is set is 2^kBias
 constexpr float kFall = 90.f;                    // octaves that a reference comes down at a time: the sums stay finite
 constexpr int kLensCache = 256;
 constexpr uint32_t kMaxDynSmem = (233472 - kCtasPerSm * 1024) / kCtasPerSm;

@@ -101,7 +101,7 @@ MQA_API mqa_status_t mqa_q8_read(void* k_out, void* v_out, const void* k_codes, 
  * Rows at or past lens[b], and rows before the window, never count, whatever
  * codes and exponents they hold.  Statistics and sums are fp32.  On the
  * tensor-core path a row's weight is off by at most 2^-9 + 2^-11 of itself and
- * less than a step of 2^-15 of the largest p_t s_t (weight times value scale),
+ * less than a step of 2^-17 of the largest p_t s_t (weight times value scale),
  * up or down as often as its size says; a query's elements by at most 2^-17 of
  * its largest.  There the value scales of one K/V head's rows, rows of zeros aside,
  * are at most 2^100 apart.

@@ -17,11 +17,11 @@ the path takes row t at, U = max_t w_t s_t):
    then to two e4m3 terms: the first is off by at most 2^-4 of its power of two,
    the second by half a step of that difference, 2^-5 2^-4 = 2^-9 of that power
    of two at most.  Below the second term's smallest step (2^-9 / 16, the largest
-   P being 2^2 or more: 2^-15 of U) it is off by less than a step, whichever way
+   P being 2^4 or more: 2^-17 of U) it is off by less than a step, whichever way
    the dither says.  Signs of v are independent of all that, so such steps add
    up as independent ones: beyond 6 standard deviations with a probability of
    2 exp(-18) (Hoeffding) each:
-       (2^-9 + 2^-11) sum_t w_t |v_t| + 6 sqrt(sum_t (2^-15 U / s_t v_t)^2).
+       (2^-9 + 2^-11) sum_t w_t |v_t| + 6 sqrt(sum_t (2^-17 U / s_t v_t)^2).
    A query's elements: 2^-10 units of which the largest has at least 224.
  - both: logits, sums and the output's rounding as in ``q8_util``."""
 import numpy as np
@@ -93,7 +93,7 @@ def within(o, q64, arrays, n, g, scale, shared):
                 t = t + A * 2 * abs(scale) * np.abs(qs).sum(1, keepdims=True) * 2.0 ** -25 * (tk * far).max()
                 t = t + 2.0 ** -25 * (w @ (tv * (sv < 2.0 ** -15 * tv)))[:, None]
             else:
-                t = t + (2.0 ** -9 + 2.0 ** -11) * A + 6 * 2.0 ** -15 * np.sqrt(step ** 2 @ aV ** 2)
+                t = t + (2.0 ** -9 + 2.0 ** -11) * A + 6 * 2.0 ** -17 * np.sqrt(step ** 2 @ aV ** 2)
                 t = t + A * 2 * 2.0 ** -10 / 224 * M
             ref[i, j * hq:(j + 1) * hq], tol[i, j * hq:(j + 1) * hq] = r, t
     assert_within(o, ref, tol, "shared" if shared else "decode")
