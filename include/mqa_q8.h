@@ -19,7 +19,8 @@
  * The library writes E in [1, 254]; rows that are attended to must not hold
  * E = 255.  A power of two costs e4m3 no precision (it is a floating format),
  * makes code * s exact in bf16 and fp32, and makes quantising what was read
- * back give the same codes and exponent again.  The exponents of one head lie in
+ * back keep every value (a row whose largest value was rounded down to 224 s
+ * gets twice the codes at half the scale).  The exponents of one head lie in
  * row order, so a tile's are one short run.
  *
  * Conventions are those of mqa.h: caller-owned device pointers on the current

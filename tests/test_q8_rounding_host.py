@@ -1,7 +1,10 @@
 """What the 8-bit tensor-core paths keep of a weight and of a query, replayed on
 the CPU number by number: the bounds that include/mqa_q8.h states hold, and
 nothing smaller does."""
+import numpy as np
 import torch
+
+from oracle import q8_oracle
 
 
 def e4m3(x):
@@ -43,3 +46,12 @@ def test_queries_in_two_e4m3_terms():
     first = e4m3(x)
     off = (first + e4m3(x - first) - x).abs()
     assert off.max() <= 2.0 ** -10 and off[x >= 0.25].max() == 0
+
+
+def test_a_row_quantised_again_may_get_other_codes_of_the_same_values():
+    """228 is nearest to 224 = 448 / 2: read back, the row fits the next smaller scale."""
+    codes, exps = q8_oracle.quantise(np.array([[228.0, 1.0, -3.5, 0.0]]))
+    val = q8_oracle.TABLE[codes] * q8_oracle.scale_of(exps)[:, None]
+    codes2, exps2 = q8_oracle.quantise(val)
+    assert exps2 == exps - 1 and val[0, 0] == 224
+    assert np.array_equal(q8_oracle.TABLE[codes2], 2 * q8_oracle.TABLE[codes])
