@@ -7,8 +7,10 @@
 // multiplication by an exact power of two, so the only rounding is the one to
 // e4m3.  Bound: HBM (2 or 4 bytes read and one written per element; the read
 // the other way round): eight bf16 prompts of up to 4,096 rows with 8 heads of
-// 128, 118 MB, are written in 20.8 us, 16 of them, 252 MB, read back in 41.7 us
-// (5.7 and 6.0 TB/s).  A decode step's few rows are bound by the launch (1.7 us).
+// 128, 118 MB, are written in 23.3 us, 16 of them, 252 MB, read back in 42.5 us
+// (5.1 and 5.9 TB/s; the prompts in 20.3 us where the L2 still holds part of
+// them).  A decode step's few rows are bound by the launch: 1.8 us in a replayed
+// graph, 4.4 in calls from Python.
 //
 // Both kernels give every thread 16 elements (32-byte loads and stores of bf16,
 // 16-byte ones of codes), so d / 16 neighbouring lanes hold a row and find its

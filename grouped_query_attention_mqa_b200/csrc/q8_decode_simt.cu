@@ -21,9 +21,12 @@
 // each: 12.9 us (25.5 with the tile kernel; 15.7 with four CTAs per SM, whose
 // registers spill).
 //
-// Otherwise q8_decode_simt_kernel.  Bound: FFMA (the codes are converted once
-// per four lanes of a row and used for all heads of the group).  Per tile, codes
-// staged by 16-byte cp.async, double buffered:
+// Otherwise q8_decode_simt_kernel.  Bound: the queries' reads of shared memory
+// and instruction issue, far from HBM (32 fp32 GQA-8 caches of 2K to 8K rows: 836
+// us, 6 TFLOP/s; bf16 at head size 64, 64 MQA caches of 1K to 8K rows with 32
+// heads: 326 us, 12 times the bf16 cache's tensor-core decode).  Per tile, codes
+// staged by 16-byte cp.async, double buffered, converted once per four lanes of a
+// row and used for all heads of the group:
 //   logits   four lanes share a row, each taking every fourth word of codes;
 //            a word becomes four floats in registers, multiplied with every
 //            head's query (16-byte broadcast reads of shared memory);
